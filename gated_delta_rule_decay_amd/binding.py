@@ -25,7 +25,10 @@ STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_SHAPE", 3: "ERR_DTYPE", 4: "ERR_UNSUPP
 EXPORTS = ("gdn2_abi_version", "gdn2_status_str", "gdn2_chunk_fwd_workspace",
            "gdn2_chunk_fwd", "gdn2_chunk_fwd_static", "gdn2_chunk_fwd_varlen_workspace", "gdn2_chunk_fwd_varlen",
            "gdn2_chunk_bwd_workspace", "gdn2_chunk_bwd", "gdn2_chunk_bwd_varlen_workspace",
-           "gdn2_chunk_bwd_varlen", "gdn2_recurrent_step")
+           "gdn2_chunk_bwd_varlen", "gdn2_recurrent_step",
+           "gdn2_linear_fwd_workspace", "gdn2_linear_fwd", "gdn2_linear_fwd_varlen_workspace", "gdn2_linear_fwd_varlen",
+           "gdn2_linear_bwd_workspace", "gdn2_linear_bwd", "gdn2_linear_bwd_varlen_workspace", "gdn2_linear_bwd_varlen",
+           "gdn2_linear_step", "gdn2_layer_norm_fwd", "gdn2_layer_norm_bwd_workspace", "gdn2_layer_norm_bwd")
 
 
 class Gdn2Desc(ctypes.Structure):

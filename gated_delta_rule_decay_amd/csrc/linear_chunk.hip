@@ -1,0 +1,996 @@
+// linear_chunk.hip -- linear attention with a decay for each head: the
+// chunked forward and backward, batched or packed sequences.
+//
+// Per (sequence, head), with a state S (dk x dv):
+//   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   a_t = exp(la_t).
+// Over a chunk of C tokens, with g the running sum of la inside the chunk and
+// S the state that enters it,
+//   o_i = scale (e^{g_i} S^T q_i + sum_{j<=i} e^{g_i-g_j} (q_i . k_j) v_j)
+//   S  <- e^{g_C} S + sum_j e^{g_C-g_j} k_j v_j^T.
+// Every exponent is a sum of decays over a forward range, so none is
+// positive and nothing has to be rescaled.
+//
+// All three gradients are the same computation on other tensors:
+//   dq_t = scale S_t dO_t           = the forward of (dO, v, k), state S^T;
+//   dv_t = dS_t^T k_t, dk_t = dS_t v_t, dS_t = a_{t+1} dS_{t+1} + scale q_t dO_t^T
+//                                   = the forward of (k, q, dO) and (v, dO, q)
+//                                     over the tokens in reverse order, where
+//                                     token t carries the decay of token t+1.
+// So one kernel, the sweep over rows (x, y, z) = (query, key, value) roles,
+// serves the forward and the backward.  The decay's gradient follows from
+//   d la_t = <S_e, dS_e> + sum_{t<=i<=e} (q_i . dq_i - k_i . dk_i)
+// for any e >= t of the sequence: the sweeps of dq and dk also store the row
+// products q.dq and k.dk, taken from their fp32 accumulators.
+//
+// Long sequences are cut into segments: a state-only sweep forms what every
+// segment adds to the state, a scan over the segments turns these into the
+// state that enters each, and the sweeps then run over all segments at once.
+#include "kernels.h"
+#include "linear.h"
+
+namespace gdn2 {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr double LOG2E = 1.4426950408889634;
+constexpr float LA_MIN = -1e4f;  // exp of anything below is 0 in fp32; keeps differences of sums finite
+
+struct SweepArgs {
+    const void *x, *y, *z;   // rows [token, H, dx], [token, H, dx], [token, H, dz]
+    void *out;               // rows [token, H, dz]
+    const void *w;           // rows [token, H, dz]: u = <w, out> per token-head (with U)
+    float *u;                // [ncb][H][tokens]
+    const float *la;
+    const float *s_in;       // [segment][H][dk*dv] or nullptr (zeros)
+    float *s_out;            // the same, or nullptr
+    double *tot;             // [segment][H]: sum of log2 decays (state-only), or nullptr
+    const int32_t *cu;       // packed sequences, one segment each (tab == nullptr)
+    const int2 *tab;         // packed sequences cut into segments: first token, end of the sequence
+    const int *nsegs;        // number of segments of a packed plan (device), or nullptr
+    int64_t T, tokens;       // tokens of a sequence (cu: of the axis), all tokens
+    int64_t segs;            // segments launched
+    int H, dx, dz;
+    int nseg, L;             // segments of a batched sequence, tokens of a segment
+    int ncb;                 // column blocks
+    int la_tok, rev;
+    int s_t;                 // state stored [dz][dx] (the sweep's state is the transpose)
+    float p_scale, u_scale, s_scale;
+};
+
+struct Seg {
+    int64_t lo, hi, end;  // tokens [lo, hi) of a sequence that ends at `end`
+};
+
+__device__ __forceinline__ Seg segment(const SweepArgs &a, int64_t seg) {
+    Seg r;
+    if (a.tab) {
+        const int2 e = a.tab[seg];
+        r.lo = e.x;
+        r.end = e.y;
+        r.hi = min(r.lo + a.L, r.end);
+    } else if (a.cu) {
+        r.lo = min(max(static_cast<int64_t>(a.cu[seg]), int64_t(0)), a.T);
+        r.hi = r.end = min(max(static_cast<int64_t>(a.cu[seg + 1]), r.lo), a.T);
+    } else {
+        const int64_t b = seg / a.nseg, s = seg - b * a.nseg;
+        r.lo = b * a.T + s * a.L;
+        r.end = (b + 1) * a.T;
+        r.hi = min(r.lo + a.L, r.end);
+    }
+    return r;
+}
+
+// Element types.  A fragment holds the 8 contraction slots of one lane for a
+// block of 32: lane group lane/16 holds slots 8 (lane/16) .. + 7, lane % 16 is
+// the other index.  The slots of a block may be in any order as long as both
+// operands use the same one.
+template <class T>
+struct Elem;
+
+template <>
+struct Elem<__bf16> {
+    using Frag = bf16x8;
+    static constexpr int CT = 64;  // tokens of a chunk
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    // x = p[0] + p[1] + .. with n parts: each part takes the next 8 bits
+    template <int N>
+    static __device__ __forceinline__ void split(const float (&x)[8], Frag (&p)[N]) {
+        float r[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const f32x2 v = {r[e], r[e + 1]};
+                const bf16x2 h = __builtin_convertvector(v, bf16x2);
+                p[i][e] = h[0];
+                p[i][e + 1] = h[1];
+                if (i + 1 < N) {
+                    r[e] -= static_cast<float>(h[0]);
+                    r[e + 1] -= static_cast<float>(h[1]);
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ float at(const Frag &f, int e) { return static_cast<float>(f[e]); }
+};
+
+template <>
+struct Elem<float> {
+    using Frag = f32x8;
+    static constexpr int CT = 32;
+    static __device__ __forceinline__ f32x4 mma(const Frag &a, const Frag &b, f32x4 c) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+    template <int N>
+    static __device__ __forceinline__ void split(const float (&x)[8], Frag (&p)[N]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[0][e] = x[e];
+    }
+    static __device__ __forceinline__ float at(const Frag &f, int e) { return f[e]; }
+};
+
+// A row-major LDS tile of COLS columns.  bf16 rows are 16-byte units permuted
+// by the row (no padding): the 16 rows of a row fragment fall in 16 different
+// units, the four rows of a transposed read in four different 64-byte windows.
+// fp32 rows are padded by 16 bytes.
+template <class T, int COLS>
+struct Tile;
+
+template <int COLS>
+struct Tile<__bf16, COLS> {
+    static_assert(COLS == 64 || COLS == 128, "8 or 16 units a row");
+    static constexpr int UNITS = COLS / 8, PER = 8, BYTES = COLS * 2;  // PER: elements of a unit
+    static __device__ __forceinline__ int unit(int row, int c) {  // byte offset of unit c of a row
+        const int f = UNITS == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+        return row * BYTES + ((c ^ f) << 4);
+    }
+    // 8 consecutive columns 8c .. of a row
+    static __device__ __forceinline__ bf16x8 row_frag(const char *t, int row, int c) {
+        return *reinterpret_cast<const bf16x8 *>(t + unit(row, c));
+    }
+    // tokens 32kt + 8g + e (e = 0..7) of the column that slot lane%16 of a
+    // 16-slot tile stands for: slot s is column `col(s/4) + s%4`, with the
+    // 4-column group of s/4 = p at half `half(p)` of unit `un(p)`.  The
+    // transposing LDS read gives lane i, element j of 16 lanes what lane
+    // 4j + i/4 addresses, element i%4.
+    static __device__ __forceinline__ bf16x8 col_frag(const char *t, int kt, int un, int half, int lane) {
+        const int row = 32 * kt + 8 * (lane >> 4) + ((lane & 15) >> 2);
+        typedef __attribute__((address_space(3))) s16x4 lds4;
+        const char *p0 = t + unit(row, un) + 8 * half, *p1 = t + unit(row + 4, un) + 8 * half;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p0);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p1);
+        const s16x8 r = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_bit_cast(bf16x8, r);
+    }
+};
+
+template <int COLS>
+struct Tile<float, COLS> {
+    static constexpr int UNITS = COLS / 4, PER = 4, BYTES = COLS * 4 + 16;
+    static __device__ __forceinline__ int unit(int row, int c) { return row * BYTES + (c << 4); }
+    static __device__ __forceinline__ f32x8 row_frag(const char *t, int row, int c) {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(t + row * BYTES + 32 * c);
+        const f32x4 b = *reinterpret_cast<const f32x4 *>(t + row * BYTES + 32 * c + 16);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    static __device__ __forceinline__ f32x8 col_frag(const char *t, int kt, int un, int half, int lane) {
+        // `un`, `half` are those of this lane's source role in the bf16 form
+        // (group lane%4); the column read here is that of group (lane%16)/4
+        const int s = lane & 15;
+        const int col = 8 * (un - (lane & 3) + (s >> 2)) + 4 * half + (s & 3);
+        const float *p = reinterpret_cast<const float *>(t + (32 * kt + 8 * (lane >> 4)) * BYTES) + col;
+        f32x8 r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = p[e * (BYTES / 4)];
+        return r;
+    }
+};
+
+// Loads of one tile, staged in registers: CT rows of COLS columns, thread by
+// thread in 16-byte units.
+template <class T, int COLS, int CT, int NTH>
+struct Stage {
+    using Tl = Tile<T, COLS>;
+    static constexpr int ALL = CT * Tl::UNITS, N = (ALL + NTH - 1) / NTH;
+    uint4 r[N];
+
+    // rows r: token base + dir * r (r < cnt), columns col0 .. of d
+    template <bool VEC>
+    __device__ __forceinline__ void load(const void *p, int64_t base, int dir, int cnt, int64_t H, int h, int d,
+                                         int col0, int tid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int f = tid + i * NTH, row = f / Tl::UNITS, c = col0 + (f % Tl::UNITS) * Tl::PER;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < cnt && c < d) {
+                const int64_t at = ((base + static_cast<int64_t>(dir) * row) * H + h) * d + c;
+                if (VEC) {
+                    v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at);
+                } else if (sizeof(T) == 2) {
+                    const uint16_t *s = static_cast<const uint16_t *>(p) + at;
+                    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < d) w[e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
+                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    const uint32_t *s = static_cast<const uint32_t *>(p) + at;
+                    v.x = s[0];
+                    if (c + 1 < d) v.y = s[1];
+                    if (c + 2 < d) v.z = s[2];
+                    if (c + 3 < d) v.w = s[3];
+                }
+            }
+            r[i] = v;
+        }
+    }
+    __device__ __forceinline__ void store(char *t, int tid) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int f = tid + i * NTH;
+            if (ALL % NTH == 0 || f < ALL)
+                *reinterpret_cast<uint4 *>(t + Tl::unit(f / Tl::UNITS, f % Tl::UNITS)) = r[i];
+        }
+    }
+};
+
+// What a sweep does: its output parts.
+constexpr int STATE = 0;  // the state only
+constexpr int OUT = 1;    // outputs (and the state)
+constexpr int OUTU = 2;   // outputs and the row products <w, out>
+
+template <class T, int DX, int NW, int NT>
+struct Shape {
+    static constexpr int CT = Elem<T>::CT, WC = NW * 16 * NT;  // columns of a workgroup
+    using TX = Tile<T, DX>;
+    using TZ = Tile<T, WC>;
+    using TP = Tile<T, sizeof(T) == 2 ? 64 : 32>;
+    static constexpr int XB = CT * TX::BYTES, ZB = CT * TZ::BYTES, PB = CT * TP::BYTES;
+    static constexpr size_t bytes(int mode, int np) {
+        return CT * 8 + 2 * CT * 4 + 16 + (mode == STATE ? 1 : 2) * XB + ZB + (mode == STATE ? 0 : np) * PB +
+               (mode == OUTU ? NW * CT * 4 : 0);
+    }
+};
+
+// One workgroup of NW waves: one segment of one head, WC columns of z.  A
+// wave holds DX x 16 NT of the state in accumulators for the whole segment:
+// tile (m, t), m = 2 ks + hf: row slot s = 4p + r is channel 32 ks + 8p + 4hf + r
+// and column slot s = 4p + r is column 8p + 4t + r of the wave's (NT = 2), so
+// that 8 contraction slots of a lane are 8 neighbouring channels, and a lane's
+// outputs 8 neighbouring columns.
+//
+// The operands made here are rounded to bf16 parts: the 64 x 64 score matrix
+// to NP of them, the state to NS, the decayed values that update the state to
+// NU (three parts hold all 24 bits; fp32 inputs are not split).
+template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU, bool VEC>
+__device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
+    using E = Elem<T>;
+    using Frag = typename E::Frag;
+    using Sh = Shape<T, DX, NW, NT>;
+    using TX = typename Sh::TX;
+    using TZ = typename Sh::TZ;
+    using TP = typename Sh::TP;
+    constexpr int CT = E::CT, KT = CT / 32, RT = CT / 16, KS = DX / 32, MT = DX / 16, NTH = 64 * NW;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, ls = lane & 15;
+    const int cb = static_cast<int>(item % a.ncb);
+    const int64_t sh = item / a.ncb;  // segment * H + head
+    const int64_t seg = sh / a.H;
+    const int h = static_cast<int>(sh - seg * a.H);
+    if (a.nsegs && seg >= *a.nsegs) return;
+    const Seg sg = segment(a, seg);
+    const int len = static_cast<int>(sg.hi - sg.lo);
+    const int col0 = cb * Sh::WC, wcol = 16 * NT * wave;  // first column of the workgroup, of the wave in it
+    const int dir = a.rev ? -1 : 1;
+    const int64_t first = a.rev ? sg.hi - 1 : sg.lo;  // token of position 0
+
+    double *s_g = reinterpret_cast<double *>(smem);
+    float *s_e = reinterpret_cast<float *>(s_g + CT);  // s_scale e^{g_i}
+    float *s_f = s_e + CT;                              // u_scale e^{g_C - g_j}
+    float *s_gam = s_f + CT;
+    char *s_y = reinterpret_cast<char *>(s_gam + 4);
+    char *s_z = s_y + Sh::XB;
+    char *s_x = s_z + Sh::ZB;
+    char *s_p = s_x + Sh::XB;
+    float *s_u = reinterpret_cast<float *>(s_p + NP * Sh::PB);  // [NW][CT]
+
+    // column of slot s of tile t, relative to the wave's
+    auto zcol = [](int t, int s) { return NT == 2 ? 8 * (s >> 2) + 4 * t + (s & 3) : s; };
+
+    f32x4 S[MT][NT];
+    const int64_t dkv = static_cast<int64_t>(a.dx) * a.dz;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            S[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (MODE != STATE && a.s_in) {
+                const int ch = 32 * (m >> 1) + 8 * g + 4 * (m & 1), col = col0 + wcol + zcol(t, ls);
+                const float *p = a.s_in + sh * dkv;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (ch + r < a.dx && col < a.dz)
+                        S[m][t][r] = a.s_t ? p[static_cast<int64_t>(col) * a.dx + ch + r]
+                                           : p[static_cast<int64_t>(ch + r) * a.dz + col];
+            }
+        }
+    if (MODE != STATE)  // the score tiles above the diagonal stay zero
+        for (int i = tid; i < NP * Sh::PB / 4; i += NTH) reinterpret_cast<uint32_t *>(s_p)[i] = 0;
+
+    Stage<T, DX, CT, NTH> sx, sy;
+    Stage<T, Sh::WC, CT, NTH> sz;
+    double total = 0.0;  // log2 decays before this chunk (wave 0)
+    float la_next = 0.f;
+    auto load_la = [&](int p) {  // decay of position p
+        float v = 0.f;
+        if (wave == 0 && lane < CT && p + lane < len) {
+            const int64_t tok = first + static_cast<int64_t>(dir) * (p + lane) + (a.rev ? 1 : 0);
+            if (tok < sg.end) v = a.la[a.la_tok ? tok * a.H + h : h];
+            if (v < LA_MIN) v = LA_MIN;
+        }
+        la_next = v;
+    };
+    auto load_tiles = [&](int p) {
+        const int64_t base = first + static_cast<int64_t>(dir) * p;
+        const int cnt = len - p;
+        sy.template load<VEC>(a.y, base, dir, cnt, a.H, h, a.dx, 0, tid);
+        sz.template load<VEC>(a.z, base, dir, cnt, a.H, h, a.dz, col0, tid);
+        if (MODE != STATE) sx.template load<VEC>(a.x, base, dir, cnt, a.H, h, a.dx, 0, tid);
+        load_la(p);
+    };
+    load_tiles(0);
+
+    for (int p0 = 0; p0 < len; p0 += CT) {
+        __syncthreads();  // the previous chunk's readers
+        sy.store(s_y, tid);
+        sz.store(s_z, tid);
+        if (MODE != STATE) sx.store(s_x, tid);
+        if (wave == 0) {
+            // running sums in 64 bits: a far reset must not cost the decays
+            // that follow it their low bits
+            double v = static_cast<double>(la_next) * LOG2E;
+#pragma unroll
+            for (int o = 1; o < CT; o <<= 1) {
+                const double up = __shfl_up(v, o);
+                if (lane >= o) v += up;
+            }
+            const double all = __shfl(v, CT - 1);
+            if (lane < CT) {
+                s_g[lane] = v;
+                s_e[lane] = a.s_scale * __builtin_amdgcn_exp2f(static_cast<float>(v));
+                s_f[lane] = a.u_scale * __builtin_amdgcn_exp2f(static_cast<float>(all - v));
+                if (lane == 0) *s_gam = __builtin_amdgcn_exp2f(static_cast<float>(all));
+            }
+            total += all;
+        }
+        __syncthreads();
+        if (p0 + CT < len) load_tiles(p0 + CT);
+
+        Frag zf[KT][NT];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int p = lane & 3;
+                if (NT == 2)
+                    zf[kt][t] = TZ::col_frag(s_z, kt, (wcol >> 3) + p, t, lane);
+                else if (sizeof(T) == 2)
+                    zf[kt][t] = TZ::col_frag(s_z, kt, (wcol >> 3) + (p >> 1), p & 1, lane);
+                else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        zf[kt][t][e] = reinterpret_cast<const float *>(s_z + (32 * kt + 8 * g + e) * TZ::BYTES)[wcol + ls];
+                }
+            }
+
+        if (MODE != STATE) {
+            // scores, transposed (rows j, columns i), so that a lane holds
+            // four neighbouring j of one i
+            constexpr int TILES = RT * (RT + 1) / 2;
+            for (int n = wave; n < TILES; n += NW) {
+                int it = 0, jt = n;
+                while (jt > it) {
+                    ++it;
+                    jt -= it;
+                }
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    acc = E::mma(TX::row_frag(s_y, 16 * jt + ls, 4 * ks + g), TX::row_frag(s_x, 16 * it + ls, 4 * ks + g), acc);
+                const int i = 16 * it + ls, j = 16 * jt + 4 * g;
+                const double gi = s_g[i];
+                float pr[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    pr[r] = j + r <= i ? acc[r] * (a.p_scale * __builtin_amdgcn_exp2f(static_cast<float>(gi - s_g[j + r])))
+                                       : 0.f;
+                if (sizeof(T) == 2) {
+                    float rest[4] = {pr[0], pr[1], pr[2], pr[3]};
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        const bf16x2 lo = __builtin_convertvector((f32x2{rest[0], rest[1]}), bf16x2);
+                        const bf16x2 hi = __builtin_convertvector((f32x2{rest[2], rest[3]}), bf16x2);
+                        const uint2 w = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+                        *reinterpret_cast<uint2 *>(s_p + q * Sh::PB + TP::unit(i, j >> 3) + 8 * (g & 1)) = w;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            rest[r] -= static_cast<float>(lo[r]);
+                            rest[2 + r] -= static_cast<float>(hi[r]);
+                        }
+                    }
+                } else {
+                    *reinterpret_cast<f32x4 *>(s_p + TP::unit(i, j >> 2)) = f32x4{pr[0], pr[1], pr[2], pr[3]};
+                }
+            }
+
+            // outputs, transposed: x S first, which needs no scores
+            f32x4 O[RT][NT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) O[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                Frag sf[NT][NS];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = S[2 * ks + (e >> 2)][t][e & 3];
+                    E::template split<NS>(v, sf[t]);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const Frag xf = TX::row_frag(s_x, 16 * rt + ls, 4 * ks + g);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) O[rt][t] = E::mma(sf[t][q], xf, O[rt][t]);
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float e = s_e[16 * rt + ls];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) O[rt][t] *= e;
+            }
+            __syncthreads();  // the scores
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+                    if (32 * kt <= 16 * rt + 15) {
+#pragma unroll
+                        for (int q = 0; q < NP; ++q) {
+                            const Frag pf = TP::row_frag(s_p + q * Sh::PB, 16 * rt + ls, 4 * kt + g);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) O[rt][t] = E::mma(zf[kt][t], pf, O[rt][t]);
+                        }
+                    }
+            // a lane's columns: NT = 2: 8g .. 8g+7 of the wave's, NT = 1: 4g .. 4g+3
+            constexpr int NC = 4 * NT;
+            const int c = col0 + wcol + NC * g;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int i = 16 * rt + ls;
+                float v[NC], us = 0.f;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[4 * t + r] = O[rt][t][r];
+                if (p0 + i < len && c < a.dz) {
+                    const int64_t at = ((first + static_cast<int64_t>(dir) * (p0 + i)) * a.H + h) * a.dz + c;
+                    T *o = static_cast<T *>(a.out) + at;
+                    if (VEC) {
+                        typedef T Tv __attribute__((ext_vector_type(4)));
+#pragma unroll
+                        for (int q = 0; q < NC; q += 4)
+                            if (NC == 4 || sizeof(T) == 2 || c + q < a.dz) {
+                                const f32x4 f = {v[q], v[q + 1], v[q + 2], v[q + 3]};
+                                *reinterpret_cast<Tv *>(o + q) = __builtin_convertvector(f, Tv);
+                            }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < NC; ++q)
+                            if (c + q < a.dz) o[q] = static_cast<T>(v[q]);
+                    }
+                    if (MODE == OUTU) {
+                        const T *w = static_cast<const T *>(a.w) + at;
+#pragma unroll
+                        for (int q = 0; q < NC; ++q)
+                            if (c + q < a.dz) us += v[q] * static_cast<float>(w[q]);
+                    }
+                }
+                if (MODE == OUTU) {
+                    us += __shfl_xor(us, 16);
+                    us += __shfl_xor(us, 32);
+                    if (g == 0) s_u[wave * CT + i] = us;
+                }
+            }
+            if (MODE == OUTU) {
+                __syncthreads();
+                if (tid < CT && p0 + tid < len) {
+                    float us = 0.f;
+#pragma unroll
+                    for (int q = 0; q < NW; ++q) us += s_u[q * CT + tid];
+                    a.u[(static_cast<int64_t>(cb) * a.H + h) * a.tokens + first + static_cast<int64_t>(dir) * (p0 + tid)] = us;
+                }
+            }
+        }
+
+        // the state: decayed, plus the chunk's products
+        const float gam = *s_gam;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S[m][t] *= gam;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            Frag zu[NT][NU];
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = s_f[32 * kt + 8 * g + e];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = f[e] * E::at(zf[kt][t], e);
+                E::template split<NU>(v, zu[t]);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const Frag yf = TX::col_frag(s_y, kt, 4 * (m >> 1) + (lane & 3), m & 1, lane);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int q = 0; q < NU; ++q) S[m][t] = E::mma(yf, zu[t][q], S[m][t]);
+            }
+        }
+    }
+
+    if (a.s_out) {
+        // in reverse order the state has yet to pass the first token's decay
+        float fin = 1.f;
+        if (MODE != STATE && a.rev && len > 0) fin = __expf(a.la[a.la_tok ? sg.lo * a.H + h : h]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int ch = 32 * (m >> 1) + 8 * g + 4 * (m & 1), col = col0 + wcol + zcol(t, ls);
+                float *p = a.s_out + sh * dkv;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (ch + r < a.dx && col < a.dz) p[static_cast<int64_t>(ch + r) * a.dz + col] = fin * S[m][t][r];
+            }
+    }
+    if (MODE == STATE && a.tot && cb == 0 && tid == 0) a.tot[sh] = total;
+}
+
+// Workgroups with neighbouring numbers run on different XCDs (eight, in
+// turn); the column blocks of one segment share its x and y rows, so they are
+// numbered to land on the same one.
+__device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t segheads, int ncb) {
+    const int64_t xcd = b & 7, q = b >> 3;
+    const int64_t sh = (q / ncb) * 8 + xcd;
+    return sh < segheads ? sh * ncb + q % ncb : -1;
+}
+__host__ int64_t xcd_blocks(int64_t segheads, int ncb) { return (segheads + 7) / 8 * 8 * ncb; }
+
+template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU, bool VEC>
+__global__ void __launch_bounds__(64 * NW) sweep_kernel(SweepArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    const int64_t item = xcd_item(blockIdx.x, a.segs * a.H, a.ncb);
+    if (item < 0) return;
+    sweep_body<T, DX, NW, NT, MODE, NP, NS, NU, VEC>(a, item, smem);
+}
+
+// The scan over a sequence's segments: what each adds to the state becomes
+// the state that enters it, in place.  One lane per state element.
+struct ScanArgs {
+    float *tab;           // [segment][H][dk*dv]
+    const double *tot;    // [segment][H]
+    const float *init;    // [N][H][dk*dv] or nullptr
+    float *fin;           // [N][H][dk*dv] or nullptr
+    const int *pfx;       // packed: segments before each sequence, or nullptr
+    const int2 *seq;      // packed: token ranges
+    const float *la;
+    int64_t N, T;
+    int64_t dkv;
+    int H, nseg, rev, la_tok, blocks;  // blocks: workgroups of a state
+};
+
+__global__ void __launch_bounds__(256) segment_scan_kernel(ScanArgs a) {
+    const int64_t sh = blockIdx.x / a.blocks, n = sh / a.H;
+    const int h = static_cast<int>(sh - n * a.H);
+    const int64_t e = static_cast<int64_t>(blockIdx.x % a.blocks) * 256 + threadIdx.x;
+    if (e >= a.dkv) return;
+    const int64_t s0 = a.pfx ? a.pfx[n] : n * a.nseg;
+    const int cnt = a.pfx ? a.pfx[n + 1] - a.pfx[n] : a.nseg;
+    float cur = a.init ? a.init[sh * a.dkv + e] : 0.f;
+    for (int i = 0; i < cnt; ++i) {
+        const int64_t sl = (s0 + (a.rev ? cnt - 1 - i : i)) * a.H + h;
+        float *p = a.tab + sl * a.dkv + e;
+        const float add = *p;
+        *p = cur;
+        cur = cur * __builtin_amdgcn_exp2f(static_cast<float>(a.tot[sl])) + add;
+    }
+    if (a.fin) {
+        const int64_t lo = a.pfx ? a.seq[n].x : n * a.T;
+        if (a.rev && cnt > 0) cur *= __expf(a.la[a.la_tok ? lo * a.H + h : h]);
+        a.fin[sh * a.dkv + e] = cur;
+    }
+}
+
+// d la of a segment: its last token's <S, dS>, then back over the segment the
+// differences of the row products, in 64 bits.  One wave per (segment, head).
+struct DecayArgs {
+    const float *uq, *uk;   // [ncb][H][tokens]
+    const float *s_tab, *d_tab;  // states entering the segments, forward and reverse
+    const float *s_fin;     // [N][H][dk*dv] final states
+    const float *la;
+    float *d_la;            // [token, H] (la_tok)
+    double *part;           // [segment][H] sums (per-head decays)
+    const int2 *tab, *seq;
+    const int *pfx;
+    int64_t N, T, tokens, segs, dkv;
+    int H, nseg, L, la_tok, nq, nk;
+};
+
+__global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs a) {
+    __shared__ double red[4];
+    const int64_t sh = blockIdx.x, seg = sh / a.H;
+    const int h = static_cast<int>(sh - seg * a.H), tid = threadIdx.x, lane = tid & 63;
+    if (a.pfx && seg >= a.pfx[a.N]) return;
+    int64_t lo, end, n;
+    bool last;
+    if (a.tab) {
+        const int2 e = a.tab[seg];
+        lo = e.x;
+        end = e.y;
+        last = lo + a.L >= end;
+        int l = 0, r = static_cast<int>(a.N) - 1;  // the sequence: the last that starts at or before seg
+        while (l < r) {
+            const int mid = (l + r + 1) >> 1;
+            if (a.pfx[mid] <= seg) l = mid;
+            else r = mid - 1;
+        }
+        n = l;
+        last = last || seg + 1 >= a.pfx[a.N];  // offsets that break the rules may cut a sequence short
+    } else {
+        n = seg / a.nseg;
+        lo = n * a.T + (seg - n * a.nseg) * a.L;
+        end = (n + 1) * a.T;
+        last = seg - n * a.nseg == a.nseg - 1;
+    }
+    const int64_t hi = min(lo + a.L, end);
+    const float *s = last ? a.s_fin + (n * a.H + h) * a.dkv : a.s_tab + (sh + a.H) * a.dkv;
+    const float *d = a.d_tab + sh * a.dkv;
+    double x = 0.0;
+    for (int64_t e = tid; e < a.dkv; e += 256) x += static_cast<double>(s[e]) * d[e];
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
+    if (lane == 0) red[tid >> 6] = x;
+    __syncthreads();
+    if (tid >= 64) return;
+    x = red[0] + red[1] + red[2] + red[3];
+    // the reverse state has yet to pass the decay behind the segment
+    if (!last) x *= exp(static_cast<double>(max(a.la[a.la_tok ? hi * a.H + h : h], LA_MIN)));
+    double sum = 0.0;
+    for (int64_t top = hi; top > lo; top -= 64) {  // tokens top-1-lane
+        const int64_t t = top - 1 - lane;
+        double v = 0.0;
+        if (t >= lo) {
+            for (int c = 0; c < a.nq; ++c) v += a.uq[(static_cast<int64_t>(c) * a.H + h) * a.tokens + t];
+            for (int c = 0; c < a.nk; ++c) v -= a.uk[(static_cast<int64_t>(c) * a.H + h) * a.tokens + t];
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double up = __shfl_up(v, o);
+            if (lane >= o) v += up;
+        }
+        if (t >= lo) {
+            if (a.la_tok) a.d_la[t * a.H + h] = static_cast<float>(x + v);
+            sum += x + v;
+        }
+        x += __shfl(v, 63);
+    }
+    if (!a.la_tok) {
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+        if (lane == 0) a.part[sh] = sum;
+    }
+}
+
+// Per-head decays: the segments' sums, always in the same order.
+__global__ void __launch_bounds__(64) decay_sum_kernel(const double *part, const int *nsegs, int64_t segs, int H,
+                                                      float *d_la) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    const int64_t n = nsegs ? *nsegs : segs;
+    double s = 0.0;
+    for (int64_t i = lane; i < n; i += 64) s += part[i * H + h];
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) d_la[h] = static_cast<float>(s);
+}
+
+// ---- host side
+
+int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+struct Cut {
+    int L;         // tokens of a segment
+    int64_t nseg;  // segments of a batched sequence
+    int64_t segs;  // segments in all (packed: the most there can be)
+};
+
+Cut cut_of(const LinArgs &a, int64_t L) {
+    Cut c;
+    c.L = static_cast<int>(L);
+    c.nseg = (a.T + L - 1) / L;
+    c.segs = a.cu ? varlen_chunk_bound(a.N, a.T, c.L) : a.N * c.nseg;
+    return c;
+}
+
+// Forward: segments only where whole sequences leave the chip empty.
+Cut fwd_cut(const LinArgs &a) {
+    const int64_t heads = a.H * (a.cu ? 1 : a.N);
+    if (a.T <= 256 || heads >= 256) return Cut{0, 1, a.N};
+    int64_t L = (a.T * heads / 512 + 63) / 64 * 64;
+    if (L < 256) L = 256;
+    if (!a.cu && L >= a.T) return Cut{0, 1, a.N};
+    return cut_of(a, L);
+}
+
+// Backward: segments of at most 1024 tokens, which also bounds how far the
+// differences of the decay's gradient are summed.
+Cut bwd_cut(const LinArgs &a) {
+    const int64_t heads = a.H * (a.cu ? 1 : a.N);
+    int64_t L = (a.T * heads / 512 + 63) / 64 * 64;
+    if (L < 256) L = 256;
+    if (L > 1024) L = 1024;
+    return cut_of(a, L);
+}
+
+template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU>
+hipError_t launch_shape(SweepArgs a, bool vec, hipStream_t s) {
+    using Sh = Shape<T, DX, NW, NT>;
+    a.ncb = (a.dz + Sh::WC - 1) / Sh::WC;
+    const int64_t blocks = xcd_blocks(a.segs * a.H, a.ncb);
+    if (blocks <= 0) return hipSuccess;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    constexpr size_t lds = Sh::bytes(MODE, NP);
+    auto go = [&](auto kernel) {
+        static_assert(lds <= 160 * 1024, "LDS of a CU");
+        if (lds > 64 * 1024) {
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(64 * NW), lds, s, a);
+        return hipGetLastError();
+    };
+    if (vec) return go(sweep_kernel<T, DX, NW, NT, MODE, NP, NS, NU, true>);
+    return go(sweep_kernel<T, DX, NW, NT, MODE, NP, NS, NU, false>);
+}
+
+// Columns of a workgroup: 128 (four waves of 32) or 64 (four of 16).
+int columns_of(int64_t dz) { return dz > 64 ? 128 : 64; }
+
+template <class T, int MODE, int NP, int NS, int NU>
+hipError_t launch_sweep(const SweepArgs &a, bool vec, hipStream_t s) {
+    if (a.dx > 64)
+        return columns_of(a.dz) == 128 ? launch_shape<T, 128, 4, 2, MODE, NP, NS, NU>(a, vec, s)
+                                       : launch_shape<T, 128, 4, 1, MODE, NP, NS, NU>(a, vec, s);
+    return columns_of(a.dz) == 128 ? launch_shape<T, 64, 4, 2, MODE, NP, NS, NU>(a, vec, s)
+                                   : launch_shape<T, 64, 4, 1, MODE, NP, NS, NU>(a, vec, s);
+}
+
+template <int MODE, int NP, int NS, int NU>
+hipError_t launch_typed(const LinArgs &l, const SweepArgs &a, bool vec, hipStream_t s) {
+    if (l.bf16) return launch_sweep<__bf16, MODE, NP, NS, NU>(a, vec, s);
+    return launch_sweep<float, MODE, 1, 1, 1>(a, vec, s);
+}
+
+SweepArgs sweep_of(const LinArgs &l, const Cut &c, const VarPlan *vp) {
+    SweepArgs a = {};
+    a.la = l.la;
+    a.T = l.T;
+    a.tokens = l.cu ? l.T : l.N * l.T;
+    a.H = static_cast<int>(l.H);
+    a.la_tok = l.la_tok;
+    a.nseg = static_cast<int>(c.nseg);
+    a.L = c.L ? c.L : static_cast<int>(l.T < 1 ? 1 : l.T);
+    a.segs = c.segs;
+    a.cu = l.cu;
+    if (vp) {
+        a.tab = vp->tab;
+        a.nsegs = vp->pfx + l.N;
+    }
+    a.p_scale = a.u_scale = a.s_scale = 1.f;
+    return a;
+}
+
+bool vector_rows(const LinArgs &l, std::initializer_list<const void *> ps) {
+    const int per = l.bf16 ? 8 : 4;
+    bool ok = l.dk % per == 0 && l.dv % per == 0;
+    for (const void *p : ps) ok = ok && aligned16(p);
+    return ok;
+}
+
+hipError_t launch_scan(ScanArgs a, hipStream_t s) {
+    a.blocks = static_cast<int>((a.dkv + 255) / 256);
+    const int64_t grid = a.N * a.H * a.blocks;
+    if (grid <= 0) return hipSuccess;
+    if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(segment_scan_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+struct Bump {
+    char *p;
+    int64_t used = 0;
+    template <class X>
+    X *take(int64_t n) {
+        X *r = p ? reinterpret_cast<X *>(p + used) : nullptr;
+        used += align256(n * static_cast<int64_t>(sizeof(X)));
+        return r;
+    }
+};
+
+struct FwdSpace {
+    float *tab;
+    double *tot;
+    char *plan;
+    int64_t bytes;
+};
+
+FwdSpace fwd_space(const LinArgs &a, const Cut &c, void *ws) {
+    Bump b{static_cast<char *>(ws)};
+    FwdSpace f = {};
+    if (c.L) {
+        f.tab = b.take<float>(c.segs * a.H * a.dk * a.dv);
+        f.tot = b.take<double>(c.segs * a.H);
+        if (a.cu) f.plan = b.take<char>(static_cast<int64_t>(varlen_plan_bytes(a.N, a.T, c.L)));
+    }
+    f.bytes = b.used;
+    return f;
+}
+
+struct BwdSpace {
+    float *s_tab, *d_tab, *s_fin, *uq, *uk;
+    double *s_tot, *d_tot, *part;
+    char *plan;
+    int64_t bytes;
+};
+
+BwdSpace bwd_space(const LinArgs &a, const Cut &c, void *ws) {
+    Bump b{static_cast<char *>(ws)};
+    BwdSpace f = {};
+    const int64_t dkv = a.dk * a.dv, tokens = a.cu ? a.T : a.N * a.T;
+    f.s_tab = b.take<float>(c.segs * a.H * dkv);
+    f.d_tab = b.take<float>(c.segs * a.H * dkv);
+    f.s_fin = b.take<float>(a.N * a.H * dkv);
+    f.s_tot = b.take<double>(c.segs * a.H);
+    f.d_tot = b.take<double>(c.segs * a.H);
+    f.part = b.take<double>(c.segs * a.H);
+    f.uq = b.take<float>((a.dk + 63) / 64 * a.H * tokens);
+    f.uk = b.take<float>((a.dk + 63) / 64 * a.H * tokens);
+    if (a.cu) f.plan = b.take<char>(static_cast<int64_t>(varlen_plan_bytes(a.N, a.T, c.L)));
+    f.bytes = b.used;
+    return f;
+}
+
+}  // namespace
+
+size_t linear_fwd_workspace(const LinArgs &a) { return static_cast<size_t>(fwd_space(a, fwd_cut(a), nullptr).bytes); }
+size_t linear_bwd_workspace(const LinArgs &a) { return static_cast<size_t>(bwd_space(a, bwd_cut(a), nullptr).bytes); }
+
+hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
+    const Cut c = ws ? fwd_cut(l) : Cut{0, 1, l.N};
+    hipError_t e;
+    VarPlan vp;
+    const FwdSpace f = fwd_space(l, c, ws);
+    const bool cut = c.L > 0;
+    if (cut && l.cu && (e = launch_varlen_plan(l.cu, l.N, l.T, c.L, f.plan, &vp, s)) != hipSuccess) return e;
+    SweepArgs a = sweep_of(l, c, cut && l.cu ? &vp : nullptr);
+    a.x = l.q;
+    a.y = l.k;
+    a.z = l.v;
+    a.dx = static_cast<int>(l.dk);
+    a.dz = static_cast<int>(l.dv);
+    a.out = l.o;
+    a.s_in = l.s0;
+    a.s_out = l.s_out;
+    const bool vec = vector_rows(l, {l.q, l.k, l.v, l.o});
+    if (cut) {
+        SweepArgs st = a;
+        st.s_in = nullptr;
+        st.s_out = f.tab;
+        st.tot = f.tot;
+        if ((e = launch_typed<STATE, 1, 1, 3>(l, st, vec, s)) != hipSuccess) return e;
+        ScanArgs sc = {f.tab, f.tot, l.s0, l.s_out, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
+                       l.dk * l.dv, a.H, a.nseg, 0, l.la_tok, 0};
+        if ((e = launch_scan(sc, s)) != hipSuccess) return e;
+        a.s_in = f.tab;
+        a.s_out = nullptr;
+    }
+    a.p_scale = a.s_scale = l.scale;
+    return launch_typed<OUT, 2, 1, 3>(l, a, vec, s);
+}
+
+hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
+    const Cut c = bwd_cut(l);
+    const BwdSpace f = bwd_space(l, c, ws);
+    hipError_t e;
+    VarPlan vp;
+    if (l.cu && (e = launch_varlen_plan(l.cu, l.N, l.T, c.L, f.plan, &vp, s)) != hipSuccess) return e;
+    const SweepArgs base = sweep_of(l, c, l.cu ? &vp : nullptr);
+    const bool vec = vector_rows(l, {l.q, l.k, l.v, l.d_o, l.dq, l.dk_out, l.dv_out});
+    const int dk = static_cast<int>(l.dk), dv = static_cast<int>(l.dv);
+
+    // what the segments add to the state, and in reverse to its gradient
+    SweepArgs a = base;
+    a.y = l.k; a.z = l.v; a.dx = dk; a.dz = dv;
+    a.s_out = f.s_tab; a.tot = f.s_tot;
+    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, vec, s)) != hipSuccess) return e;
+    a.y = l.q; a.z = l.d_o; a.rev = 1; a.u_scale = l.scale;
+    a.s_out = f.d_tab; a.tot = f.d_tot;
+    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, vec, s)) != hipSuccess) return e;
+    ScanArgs sc = {f.s_tab, f.s_tot, l.s0, f.s_fin, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
+                   l.dk * l.dv, base.H, base.nseg, 0, l.la_tok, 0};
+    if ((e = launch_scan(sc, s)) != hipSuccess) return e;
+    sc.tab = f.d_tab; sc.tot = f.d_tot; sc.init = l.d_sT; sc.fin = l.d_s0; sc.rev = 1;
+    if ((e = launch_scan(sc, s)) != hipSuccess) return e;
+
+    // dq
+    a = base;
+    a.x = l.d_o; a.y = l.v; a.z = l.k; a.dx = dv; a.dz = dk;
+    a.out = l.dq; a.w = l.q; a.u = f.uq;
+    a.s_in = f.s_tab; a.s_t = 1;
+    a.p_scale = a.s_scale = l.scale;
+    if ((e = launch_typed<OUTU, 3, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
+    // dk
+    a.x = l.v; a.y = l.d_o; a.z = l.q;
+    a.out = l.dk_out; a.w = l.k; a.u = f.uk;
+    a.s_in = f.d_tab; a.rev = 1;
+    a.p_scale = a.u_scale = l.scale;
+    a.s_scale = 1.f;
+    if ((e = launch_typed<OUTU, 3, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
+    // dv
+    a.x = l.k; a.y = l.q; a.z = l.d_o; a.dx = dk; a.dz = dv;
+    a.out = l.dv_out; a.w = nullptr; a.u = nullptr;
+    a.s_t = 0;
+    if ((e = launch_typed<OUT, 2, 1, 2>(l, a, vec, s)) != hipSuccess) return e;
+
+    const int ncb = (dk + columns_of(dk) - 1) / columns_of(dk);
+    DecayArgs d = {f.uq, f.uk, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,
+                   l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,
+                   base.nseg, c.L, l.la_tok, ncb, ncb};
+    if (c.segs * l.H > 0) {
+        hipLaunchKernelGGL(decay_grad_kernel, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(256), 0, s, d);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!l.la_tok) {
+        hipLaunchKernelGGL(decay_sum_kernel, dim3(static_cast<unsigned>(l.H)), dim3(64), 0, s, f.part,
+                           l.cu ? vp.pfx + l.N : nullptr, c.segs, base.H, l.d_la);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace gdn2

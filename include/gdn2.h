@@ -363,6 +363,171 @@ gdn2_status gdn2_recurrent_step(const gdn2_desc *desc,
                                 const float *log_decay, const float *erase, const float *write,
                                 float *state, float *o, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the token mixer without the
+ * erase step, beside the gated delta rule.  Per (batch, head), with a state
+ * S in R^{dk x dv} (key-by-value, as above):
+ *
+ *     S_t = a_t S_{t-1} + k_t v_t^T          a_t = exp(log_decay_t)
+ *     o_t = q_scale S_t^T q_t                read after the update
+ *
+ * The delta rule with b = 0, w = 1 and a per-head decay is the same
+ * recurrence; these calls do not pay for its triangular solve, take q, k, v
+ * of any finite size (no fp16 anywhere) and decays that are one value per
+ * token and head or one per head.
+ *
+ * Conventions are those at the top of this file: contiguous device tensors,
+ * host-side validation before anything is enqueued, work on `stream`, no
+ * allocation, no synchronisation.  Outputs and gradients of q, k, v have
+ * the type of q, k, v (bf16 results are the fp32 ones rounded once, to
+ * nearest even); states, decays and their gradients are fp32.
+ *
+ * Precision, bf16 inputs: the products of inputs are exact, every sum is
+ * fp32.  The masked scores enter their product as two bf16 parts (16 bits),
+ * the state enters the read as one bf16 (8 bits: about one more rounding of
+ * the output's size), and the values that update the state as three (all 24
+ * bits), so the states carry fp32 accuracy, as do d_log_decay and d_state0.
+ * fp32 inputs: fp32 throughout.
+ *
+ * Preconditions not checked: all values finite, log_decay <= 0 (minus
+ * infinity is allowed and clears the state; anything below -10000 counts as
+ * -10000, whose exponential is 0).
+ */
+typedef enum gdn2_decay_kind {
+    GDN2_DECAY_TOKEN = 0, /* log_decay [B,T,H]: one value per token and head */
+    GDN2_DECAY_HEAD = 1   /* log_decay [H]: one value per head               */
+} gdn2_decay_kind;
+
+typedef struct gdn2_linear_desc {
+    int64_t batch;      /* B >= 0 (packed: N sequences)            */
+    int64_t seqlen;     /* T >= 0 (packed: tokens of the one axis) */
+    int64_t heads;      /* H >= 1 */
+    int64_t dk;         /* key channels,   1..128 */
+    int64_t dv;         /* value channels, 1..128 */
+    int32_t dtype;      /* gdn2_dtype of q, k, v, o, d_o and the gradients of q, k, v */
+    int32_t decay_kind; /* gdn2_decay_kind */
+    float q_scale;      /* multiplies q */
+    int32_t reserved;   /* 0 */
+} gdn2_linear_desc;
+
+/* Device workspace, in bytes, with which gdn2_linear_fwd runs long
+ * sequences on few chains in parallel segments; 0 where whole chains fill
+ * the GPU.  It holds one fp32 state per (segment, head). */
+gdn2_status gdn2_linear_fwd_workspace(const gdn2_linear_desc *desc, size_t *bytes);
+
+/*
+ * Chunked forward over whole sequences (training / prefill).
+ *
+ *   q, k [B,T,H,dk], v [B,T,H,dv]; log_decay fp32 per desc->decay_kind
+ *   state0       initial state [B,H,dk,dv] fp32, or NULL for zeros
+ *   o            [B,T,H,dv], must not overlap any input
+ *   state_out    final state [B,H,dk,dv] fp32, or NULL; it may be exactly
+ *                state0 (in place), any other overlap is GDN2_ERR_ALIAS
+ *   workspace    NULL (or ws_bytes 0): one pass over each chain, no scratch;
+ *                otherwise >= gdn2_linear_fwd_workspace() bytes, 256-byte
+ *                aligned (GDN2_ERR_WORKSPACE), overlapping nothing else.
+ *                Calls that share one must not overlap in time.
+ * T == 0: state_out receives state0 (or zeros), nothing else is touched.
+ */
+gdn2_status gdn2_linear_fwd(const gdn2_linear_desc *desc, const void *q, const void *k, const void *v,
+                            const float *log_decay, const float *state0, void *o, float *state_out,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/* As gdn2_linear_fwd_workspace, for gdn2_linear_fwd_varlen. */
+gdn2_status gdn2_linear_fwd_varlen_workspace(const gdn2_linear_desc *desc, size_t *bytes);
+
+/*
+ * The forward over N = desc->batch sequences packed along one axis of T =
+ * desc->seqlen tokens (q, k [T,H,dk], v, o [T,H,dv], log_decay [T,H] or [H],
+ * states [N,H,dk,dv]).  cu_seqlens: DEVICE int32 [N+1], 0 = cu[0] <= .. <=
+ * cu[N] = T, not checked but clamped as for gdn2_chunk_fwd_varlen, so no
+ * access leaves the buffers.  Rows outside every sequence are untouched; an
+ * empty sequence passes its state through.
+ */
+gdn2_status gdn2_linear_fwd_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens,
+                                   const void *q, const void *k, const void *v,
+                                   const float *log_decay, const float *state0, void *o, float *state_out,
+                                   void *workspace, size_t ws_bytes, void *stream);
+
+/* Device workspace, in bytes, for gdn2_linear_bwd: two fp32 states per
+ * (segment of up to 1024 tokens, head), one per chain, and a few fp32 values
+ * per token-head. */
+gdn2_status gdn2_linear_bwd_workspace(const gdn2_linear_desc *desc, size_t *bytes);
+
+/*
+ * Backward of gdn2_linear_fwd: the gradients of <d_o, o> + <d_state_out, S_T>.
+ *
+ *   q .. state0  the forward's inputs; d_o like o
+ *   d_state_out  [B,H,dk,dv] fp32, or NULL for zeros
+ *   dq, dk, dv   like q, k, v
+ *   d_log_decay  fp32, like log_decay (per head: summed over tokens and
+ *                sequences, in a fixed order)
+ *   d_state0     [B,H,dk,dv] fp32, or NULL to skip
+ *   workspace    >= gdn2_linear_bwd_workspace() bytes, 256-byte aligned
+ * Outputs must not overlap each other, any input or the workspace.  The
+ * result is the same, bit for bit, on every run.  T == 0 (or B == 0):
+ * d_state0 receives d_state_out (or zeros), a per-head d_log_decay zeros.
+ */
+gdn2_status gdn2_linear_bwd(const gdn2_linear_desc *desc, const void *q, const void *k, const void *v,
+                            const float *log_decay, const float *state0, const void *d_o,
+                            const float *d_state_out, void *dq, void *dk, void *dv, float *d_log_decay,
+                            float *d_state0, void *workspace, size_t ws_bytes, void *stream);
+
+/* As gdn2_linear_bwd_workspace, for gdn2_linear_bwd_varlen. */
+gdn2_status gdn2_linear_bwd_varlen_workspace(const gdn2_linear_desc *desc, size_t *bytes);
+
+/* Backward of gdn2_linear_fwd_varlen; rows of dq, dk, dv and of a per-token
+ * d_log_decay outside every sequence are untouched. */
+gdn2_status gdn2_linear_bwd_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens,
+                                   const void *q, const void *k, const void *v, const float *log_decay,
+                                   const float *state0, const void *d_o, const float *d_state_out,
+                                   void *dq, void *dk, void *dv, float *d_log_decay, float *d_state0,
+                                   void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One decode step for N = desc->batch sequences (desc->seqlen must be 1):
+ * q, k [N,H,dk], v [N,H,dv], log_decay [N,H] or [H]; state [N,H,dk,dv] fp32
+ * is read and rewritten in place; o [N,H,dv].  fp32 arithmetic.
+ */
+gdn2_status gdn2_linear_step(const gdn2_linear_desc *desc, const void *q, const void *k, const void *v,
+                             const float *log_decay, float *state, void *o, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm over the last axis, which normalises a mixer's output per head
+ * or a block's input over the model width:
+ *
+ *     y = (x - mean) rstd * weight + bias,   rstd = 1 / sqrt(var + eps)
+ *
+ * Rows [rows, dim] of bf16 or fp32; weight and bias [groups, dim] (fp32 or
+ * bf16, one type), row r taking row r % groups: groups = 1 shares them, and
+ * groups = H with rows of [B,T,H,dim] gives each head its own.  All sums are
+ * fp32 (over rows: then fp64), results rounded once.  dim 1..16384.
+ */
+typedef struct gdn2_norm_desc {
+    int64_t rows;         /* >= 0, a multiple of groups */
+    int64_t groups;       /* >= 1 */
+    int64_t dim;          /* 1..16384 */
+    int32_t dtype;        /* gdn2_dtype of x, y, dy, dx */
+    int32_t weight_dtype; /* gdn2_dtype of weight, bias and their gradients */
+    float eps;            /* >= 0 */
+    int32_t reserved;     /* 0 */
+} gdn2_norm_desc;
+
+/* weight NULL: ones; bias NULL: zeros.  mean, rstd: fp32 [rows], what the
+ * backward needs, or NULL.  Outputs overlap nothing else. */
+gdn2_status gdn2_layer_norm_fwd(const gdn2_norm_desc *desc, const void *x, const void *weight, const void *bias,
+                                void *y, float *mean, float *rstd, void *stream);
+
+/* Device workspace, in bytes, for the row sums of gdn2_layer_norm_bwd. */
+gdn2_status gdn2_layer_norm_bwd_workspace(const gdn2_norm_desc *desc, size_t *bytes);
+
+/* Gradients of <dy, y>: dx [rows, dim]; d_weight, d_bias [groups, dim]
+ * (either may be NULL), each summed in a fixed order.  The workspace
+ * (256-byte aligned) may be NULL when both are.  rows == 0: the sums are 0. */
+gdn2_status gdn2_layer_norm_bwd(const gdn2_norm_desc *desc, const void *dy, const void *x, const void *weight,
+                                const float *mean, const float *rstd, void *dx, void *d_weight, void *d_bias,
+                                void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
