@@ -71,7 +71,8 @@ gdn2_status check_linear(const gdn2_linear_desc *d, bool packed) {
         return GDN2_ERR_SHAPE;
     // launch sizes: 64 workgroups a state, two a segment of 256 tokens
     const int64_t chains = d->batch * d->heads, rows = (packed ? 1 : d->batch) * d->heads;
-    if (d->seqlen > INT32_MAX || chains > (INT32_MAX >> 6) || d->heads > (INT32_MAX >> 6) ||
+    if (d->seqlen > INT32_MAX || chains > (INT32_MAX >> 6) || d->heads > 65535 ||  // 32-bit offsets inside a chunk
+       
         rows > (INT64_C(1) << 62) / (d->seqlen / 256 + 1) ||
         2 * (rows * (d->seqlen / 256 + 1) + chains + 8) > INT32_MAX)
         return GDN2_ERR_UNSUPPORTED;

@@ -36,6 +36,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -45,8 +47,8 @@ constexpr float LA_MIN = -1e4f;  // exp of anything below is 0 in fp32; keeps di
 struct SweepArgs {
     const void *x, *y, *z;   // rows [token, H, dx], [token, H, dx], [token, H, dz]
     void *out;               // rows [token, H, dz]
-    const void *w;           // rows [token, H, dz]: u = <w, out> per token-head (with U)
-    float *u;                // [ncb][H][tokens]
+    const void *w;           // rows [token, H, dz], for u
+    float *u;                // [H][tokens]
     const float *la;
     const float *s_in;       // [segment][H][dk*dv] or nullptr (zeros)
     float *s_out;            // the same, or nullptr
@@ -143,9 +145,9 @@ struct Elem<float> {
 };
 
 // A row-major LDS tile of COLS columns.  bf16 rows are 16-byte units permuted
-// by the row (no padding): the 16 rows of a row fragment fall in 16 different
-// units, the four rows of a transposed read in four different 64-byte windows.
-// fp32 rows are padded by 16 bytes.
+// by the row (no padding), so that the 16 rows of a row fragment fall in 16
+// different units; a transposed read then takes its banks twice.  fp32 rows
+// are padded by 16 bytes.
 template <class T, int COLS>
 struct Tile;
 
@@ -154,26 +156,32 @@ struct Tile<__bf16, COLS> {
     static_assert(COLS == 64 || COLS == 128, "8 or 16 units a row");
     static constexpr int UNITS = COLS / 8, PER = 8, BYTES = COLS * 2;  // PER: elements of a unit
     static __device__ __forceinline__ int unit(int row, int c) {  // byte offset of unit c of a row
-        const int f = UNITS == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+        const int f = UNITS == 16 ? ((row & 1) << 2) | ((row >> 1) & 3) | (row & 8) : (row >> 1) & 7;
         return row * BYTES + ((c ^ f) << 4);
     }
     // 8 consecutive columns 8c .. of a row
     static __device__ __forceinline__ bf16x8 row_frag(const char *t, int row, int c) {
         return *reinterpret_cast<const bf16x8 *>(t + unit(row, c));
     }
-    // tokens 32kt + 8g + e (e = 0..7) of the column that slot lane%16 of a
-    // 16-slot tile stands for: slot s is column `col(s/4) + s%4`, with the
-    // 4-column group of s/4 = p at half `half(p)` of unit `un(p)`.  The
-    // transposing LDS read gives lane i, element j of 16 lanes what lane
-    // 4j + i/4 addresses, element i%4.
+    // Tokens 32 kt + 8g + e (e = 0..7) of the column that slot lane%16 of a
+    // 16-slot tile stands for: slots 4p .. 4p+3 are the 4 columns at half
+    // `half` of unit `un`, both given for p = lane%4.  The transposing LDS
+    // read gives lane i, element j of 16 lanes what lane 4j + i/4 addresses,
+    // element i%4.
     static __device__ __forceinline__ bf16x8 col_frag(const char *t, int kt, int un, int half, int lane) {
-        const int row = 32 * kt + 8 * (lane >> 4) + ((lane & 15) >> 2);
+        const int row = 8 * (lane >> 4) + ((lane & 15) >> 2);
         typedef __attribute__((address_space(3))) s16x4 lds4;
-        const char *p0 = t + unit(row, un) + 8 * half, *p1 = t + unit(row + 4, un) + 8 * half;
+        const char *p0 = t + 32 * kt * BYTES + unit(row, un) + 8 * half;
+        const char *p1 = t + 32 * kt * BYTES + unit(row + 4, un) + 8 * half;
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p0);
         const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p1);
         const s16x8 r = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         return __builtin_bit_cast(bf16x8, r);
+    }
+    // the 4 columns 4c .. of a row
+    static __device__ __forceinline__ f32x4 quad(const char *t, int row, int c) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(t + unit(row, c >> 1) + 8 * (c & 1)), f32x4);
     }
 };
 
@@ -186,82 +194,183 @@ struct Tile<float, COLS> {
         const f32x4 b = *reinterpret_cast<const f32x4 *>(t + row * BYTES + 32 * c + 16);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
+    // `un`, `half` as in the bf16 form: given for group lane%4, where the
+    // column read here is one of group (lane%16)/4
     static __device__ __forceinline__ f32x8 col_frag(const char *t, int kt, int un, int half, int lane) {
-        // `un`, `half` are those of this lane's source role in the bf16 form
-        // (group lane%4); the column read here is that of group (lane%16)/4
         const int s = lane & 15;
-        const int col = 8 * (un - (lane & 3) + (s >> 2)) + 4 * half + (s & 3);
+        return column(t, kt, 8 * (un - (lane & 3) + (s >> 2)) + 4 * half + (s & 3), lane);
+    }
+    static __device__ __forceinline__ f32x8 column(const char *t, int kt, int col, int lane) {
         const float *p = reinterpret_cast<const float *>(t + (32 * kt + 8 * (lane >> 4)) * BYTES) + col;
         f32x8 r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[e] = p[e * (BYTES / 4)];
         return r;
     }
+    static __device__ __forceinline__ f32x4 quad(const char *t, int row, int c) {
+        return *reinterpret_cast<const f32x4 *>(t + unit(row, c));
+    }
 };
 
-// Loads of one tile, staged in registers: CT rows of COLS columns, thread by
-// thread in 16-byte units.
-template <class T, int COLS, int CT, int NTH>
+// The score matrix: blocks of 32 columns (tokens j), block kt with the rows
+// i >= 32 kt, each row 32 elements.
+template <class T>
+struct Scores;
+
+template <>
+struct Scores<__bf16> {
+    static constexpr int ROW = 64, BYTES = (64 + 32) * ROW;
+    static __device__ __forceinline__ int at(int kt, int row, int c) {  // unit c (8 columns) of a row of block kt
+        return kt * (32 * ROW) + row * ROW + ((c ^ ((row >> 2) & 3)) << 4);
+    }
+    static __device__ __forceinline__ bf16x8 frag(const char *p, int kt, int row, int g) {
+        return *reinterpret_cast<const bf16x8 *>(p + at(kt, row, g));
+    }
+};
+
+template <>
+struct Scores<float> {
+    static constexpr int ROW = 32 * 4 + 16, BYTES = 32 * ROW;
+    static __device__ __forceinline__ int at(int, int row, int c) { return row * ROW + (c << 4); }  // 4 columns
+    static __device__ __forceinline__ f32x8 frag(const char *p, int, int row, int g) {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(p + row * ROW + 32 * g);
+        const f32x4 b = *reinterpret_cast<const f32x4 *>(p + row * ROW + 32 * g + 16);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// Buffer accesses: a uniform base, a 32-bit lane offset and a uniform one,
+// where an offset of NOWHERE reads zeros and stores nothing.
+constexpr int NOWHERE = -1;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int bytes = 0x7fffffff) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((static_cast<uint64_t>(hi) << 32) | lo), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, int off, int add) {
+    return __builtin_amdgcn_raw_buffer_load_b128(b, off, add, 0);
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t b, int off, int add) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, off, add, 0));
+}
+__device__ __forceinline__ void store4(float v, __amdgpu_buffer_rsrc_t b, int off, int add) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b, off, add, 0);
+}
+
+// Rows of one tensor for the chunks of a segment, staged in registers: CT
+// rows of COLS columns, thread by thread in 16-byte units.  Positions run
+// forward from token `first`, or (rev) back from it.
+template <class T, int COLS, int CT, int NTH, bool VEC>
 struct Stage {
     using Tl = Tile<T, COLS>;
-    static constexpr int ALL = CT * Tl::UNITS, N = (ALL + NTH - 1) / NTH;
-    uint4 r[N];
+    static constexpr int RX = NTH / Tl::UNITS, N = CT / RX;  // rows of a pass, passes
+    static_assert(RX <= CT && CT % RX == 0 && (sizeof(T) == 4 || RX % 16 == 0), "whole passes, of one permutation");
+    u32x4 r[N];
+    const T *base;  // row of position 0, column 0 of the head
+    int64_t row;    // elements from one token to the next
+    int off;        // this thread's bytes in pass 0 (rev: in the last)
+    int r0, c, d;
+    bool rev;
 
-    // rows r: token base + dir * r (r < cnt), columns col0 .. of d
-    template <bool VEC>
-    __device__ __forceinline__ void load(const void *p, int64_t base, int dir, int cnt, int64_t H, int h, int d,
-                                         int col0, int tid) {
+    __device__ __forceinline__ void init(const void *p, int64_t first, int64_t H, int h, int d_, int col0, bool rev_, int tid) {
+        d = d_;
+        rev = rev_;
+        row = H * d;
+        base = static_cast<const T *>(p) + (first * H + h) * d;
+        r0 = tid / Tl::UNITS;
+        c = col0 + (tid % Tl::UNITS) * Tl::PER;
+        const int at = rev ? RX - 1 - r0 : r0;
+        off = c < d ? (at * static_cast<int>(row) + c) * static_cast<int>(sizeof(T)) : NOWHERE;
+    }
+    // positions p0 .. p0+CT-1, of which [0, len) exist
+    __device__ __forceinline__ void load(int p0, int len) {
+        if (VEC) {
+            const auto b = buffer(base + (rev ? -(p0 + CT - 1) : p0) * row);
+            const bool full = p0 >= 0 && p0 + CT <= len;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int f = tid + i * NTH, row = f / Tl::UNITS, c = col0 + (f % Tl::UNITS) * Tl::PER;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < cnt && c < d) {
-                const int64_t at = ((base + static_cast<int64_t>(dir) * row) * H + h) * d + c;
-                if (VEC) {
-                    v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at);
-                } else if (sizeof(T) == 2) {
-                    const uint16_t *s = static_cast<const uint16_t *>(p) + at;
-                    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (c + e < d) w[e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
-                    v = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-                    const uint32_t *s = static_cast<const uint32_t *>(p) + at;
-                    v.x = s[0];
-                    if (c + 1 < d) v.y = s[1];
-                    if (c + 2 < d) v.z = s[2];
-                    if (c + 3 < d) v.w = s[3];
-                }
+            for (int i = 0; i < N; ++i) {
+                const int p = p0 + r0 + i * RX;
+                r[i] = load16(b, full || (p >= 0 && p < len) ? off : NOWHERE,
+                              (rev ? N - 1 - i : i) * RX * static_cast<int>(row) * static_cast<int>(sizeof(T)));
             }
-            r[i] = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int p = p0 + r0 + i * RX;
+                u32x4 v = {0, 0, 0, 0};
+                if (p >= 0 && p < len && c < d) {
+                    const T *s = base + (rev ? -p : p) * row + c;
+                    if (sizeof(T) == 2) {
+                        const uint16_t *e = reinterpret_cast<const uint16_t *>(s);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (c + k < d) v[k >> 1] |= static_cast<uint32_t>(e[k]) << (16 * (k & 1));
+                    } else {
+                        const uint32_t *e = reinterpret_cast<const uint32_t *>(s);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (c + k < d) v[k] = e[k];
+                    }
+                }
+                r[i] = v;
+            }
         }
     }
     __device__ __forceinline__ void store(char *t, int tid) const {
+        const int at = Tl::unit(r0, tid % Tl::UNITS);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int f = tid + i * NTH;
-            if (ALL % NTH == 0 || f < ALL)
-                *reinterpret_cast<uint4 *>(t + Tl::unit(f / Tl::UNITS, f % Tl::UNITS)) = r[i];
-        }
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(t + at + i * RX * Tl::BYTES) = r[i];
     }
 };
+
+// Sum of v over this lane and the lower lanes of the wave, in 64 bits.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, false);
+    return v + __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+__device__ __forceinline__ double wave_prefix(double v) {
+    v = dpp_add<0x111, 0xf>(v);  // one, two, four, eight lanes up within rows of 16
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);  // a row's last lane to the next row
+    return dpp_add<0x143, 0xc>(v);  // the lower half's last lane to the upper half
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
+    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+// Sum over the 16 lanes of a row, in its last lane.
+__device__ __forceinline__ float row16_sum(float v) {
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x111, 0xf, 0xf, false));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x112, 0xf, 0xf, false));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x114, 0xf, 0xf, false));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x118, 0xf, 0xf, false));
+    return v;
+}
 
 // What a sweep does: its output parts.
 constexpr int STATE = 0;  // the state only
 constexpr int OUT = 1;    // outputs (and the state)
-constexpr int OUTU = 2;   // outputs and the row products <w, out>
+constexpr int OUTU = 2;   // outputs and u, the read's row products <w, x S>
+constexpr int OUTM = 3;   // OUTU, and in u what the pairs inside a chunk add
 
 template <class T, int DX, int NW, int NT>
 struct Shape {
     static constexpr int CT = Elem<T>::CT, WC = NW * 16 * NT;  // columns of a workgroup
     using TX = Tile<T, DX>;
     using TZ = Tile<T, WC>;
-    using TP = Tile<T, sizeof(T) == 2 ? 64 : 32>;
-    static constexpr int XB = CT * TX::BYTES, ZB = CT * TZ::BYTES, PB = CT * TP::BYTES;
+    static constexpr int XB = CT * TX::BYTES, ZB = CT * TZ::BYTES;
     static constexpr size_t bytes(int mode, int np) {
-        return CT * 8 + 2 * CT * 4 + 16 + (mode == STATE ? 1 : 2) * XB + ZB + (mode == STATE ? 0 : np) * PB +
-               (mode == OUTU ? NW * CT * 4 : 0);
+        return CT * 8 + 2 * CT * 4 + 16 + (mode == STATE ? 1 : 2) * XB + (mode >= OUTU ? 2 : 1) * ZB +
+               (mode == STATE ? 0 : np * Scores<T>::BYTES) + (mode >= OUTU ? NW * CT * 4 : 0) +
+               (mode == OUTM ? (CT / 16 + 1) * CT * 4 : 0);
     }
 };
 
@@ -272,30 +381,39 @@ struct Shape {
 // that 8 contraction slots of a lane are 8 neighbouring channels, and a lane's
 // outputs 8 neighbouring columns.
 //
-// The operands made here are rounded to bf16 parts: the 64 x 64 score matrix
-// to NP of them, the state to NS, the decayed values that update the state to
-// NU (three parts hold all 24 bits; fp32 inputs are not split).
+// The operands made here are rounded to bf16 parts: the score matrix to NP of
+// them, the state to NS, the decayed values that update the state to NU (three
+// parts hold all 24 bits; fp32 inputs are not split).
+//
+// OUTU and OUTM (all of z's columns in one workgroup): per token the part of
+// the decay's gradient that it opens or closes,
+//   u_i = <w_i, e^{g_i} S^T x_i>  [+ sum_{j<i} M_ij - sum_{j>i} M_ji],
+//   M_ij = (score i, j) (w_i . z_j):
+// pairs inside a chunk enter both their ends with the same fp32 value, so the
+// sum over a chunk's tail keeps their precision.
 template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU, bool VEC>
-__device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
+__device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
     using E = Elem<T>;
     using Frag = typename E::Frag;
     using Sh = Shape<T, DX, NW, NT>;
     using TX = typename Sh::TX;
     using TZ = typename Sh::TZ;
-    using TP = typename Sh::TP;
+    using Sc = Scores<T>;
     constexpr int CT = E::CT, KT = CT / 32, RT = CT / 16, KS = DX / 32, MT = DX / 16, NTH = 64 * NW;
+    constexpr int ESZ = sizeof(T);
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, ls = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, ls = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int cb = static_cast<int>(item % a.ncb);
     const int64_t sh = item / a.ncb;  // segment * H + head
     const int64_t seg = sh / a.H;
     const int h = static_cast<int>(sh - seg * a.H);
     if (a.nsegs && seg >= *a.nsegs) return;
     const Seg sg = segment(a, seg);
-    const int len = static_cast<int>(sg.hi - sg.lo);
+    const int len = __builtin_amdgcn_readfirstlane(static_cast<int>(sg.hi - sg.lo));
     const int col0 = cb * Sh::WC, wcol = 16 * NT * wave;  // first column of the workgroup, of the wave in it
-    const int dir = a.rev ? -1 : 1;
-    const int64_t first = a.rev ? sg.hi - 1 : sg.lo;  // token of position 0
+    const bool rev = a.rev;
+    const int64_t first = rev ? sg.hi - 1 : sg.lo;  // token of position 0
 
     double *s_g = reinterpret_cast<double *>(smem);
     float *s_e = reinterpret_cast<float *>(s_g + CT);  // s_scale e^{g_i}
@@ -305,126 +423,150 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
     char *s_z = s_y + Sh::XB;
     char *s_x = s_z + Sh::ZB;
     char *s_p = s_x + Sh::XB;
-    float *s_u = reinterpret_cast<float *>(s_p + NP * Sh::PB);  // [NW][CT]
+    char *s_w = s_p + NP * Sc::BYTES;
+    float *s_u = reinterpret_cast<float *>(s_w + Sh::ZB);  // [NW][CT]
+    float *s_m = s_u + NW * CT;  // [CT/16 blocks][CT/16 + 1][16]: row sums of the block's tiles, then column sums
 
     // column of slot s of tile t, relative to the wave's
     auto zcol = [](int t, int s) { return NT == 2 ? 8 * (s >> 2) + 4 * t + (s & 3) : s; };
 
+    // the state's elements of this lane: channels 32 ks + 4 hf + 8g + r
     f32x4 S[MT][NT];
-    const int64_t dkv = static_cast<int64_t>(a.dx) * a.dz;
+    const int dkv = a.dx * a.dz;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            S[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (MODE != STATE && a.s_in) {
-                const int ch = 32 * (m >> 1) + 8 * g + 4 * (m & 1), col = col0 + wcol + zcol(t, ls);
-                const float *p = a.s_in + sh * dkv;
+        for (int t = 0; t < NT; ++t) S[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bool all_ch = a.dx == DX;
+    int soff[NT];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (ch + r < a.dx && col < a.dz)
-                        S[m][t][r] = a.s_t ? p[static_cast<int64_t>(col) * a.dx + ch + r]
-                                           : p[static_cast<int64_t>(ch + r) * a.dz + col];
+    for (int t = 0; t < NT; ++t) {
+        const int col = col0 + wcol + zcol(t, ls);
+        soff[t] = col < a.dz ? 4 * (8 * g * a.dz + col) : NOWHERE;
+    }
+    if (MODE != STATE && a.s_in) {
+        const auto b = buffer(a.s_in + sh * dkv, 4 * dkv);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int ch = 32 * (m >> 1) + 4 * (m & 1);
+                if (!a.s_t) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        S[m][t][r] = load4(b, all_ch || ch + 8 * g + r < a.dx ? soff[t] : NOWHERE, 4 * (ch + r) * a.dz);
+                } else {
+                    const int col = col0 + wcol + zcol(t, ls);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int c = ch + 8 * g + r;
+                        S[m][t][r] = load4(b, c < a.dx && col < a.dz ? 4 * (col * a.dx + c) : NOWHERE, 0);
+                    }
+                }
             }
-        }
+    }
     if (MODE != STATE)  // the score tiles above the diagonal stay zero
-        for (int i = tid; i < NP * Sh::PB / 4; i += NTH) reinterpret_cast<uint32_t *>(s_p)[i] = 0;
+        for (int i = tid; i < NP * Sc::BYTES / 4; i += NTH) reinterpret_cast<uint32_t *>(s_p)[i] = 0;
 
-    Stage<T, DX, CT, NTH> sx, sy;
-    Stage<T, Sh::WC, CT, NTH> sz;
+    Stage<T, DX, CT, NTH, VEC> sx, sy;
+    Stage<T, Sh::WC, CT, NTH, VEC> sz, sw;
+    sy.init(a.y, first, a.H, h, a.dx, 0, rev, tid);
+    sz.init(a.z, first, a.H, h, a.dz, col0, rev, tid);
+    if (MODE != STATE) sx.init(a.x, first, a.H, h, a.dx, 0, rev, tid);
+    if (MODE >= OUTU) sw.init(a.w, first, a.H, h, a.dz, col0, rev, tid);
     double total = 0.0;  // log2 decays before this chunk (wave 0)
     float la_next = 0.f;
-    auto load_la = [&](int p) {  // decay of position p
-        float v = 0.f;
-        if (wave == 0 && lane < CT && p + lane < len) {
-            const int64_t tok = first + static_cast<int64_t>(dir) * (p + lane) + (a.rev ? 1 : 0);
-            if (tok < sg.end) v = a.la[a.la_tok ? tok * a.H + h : h];
-            if (v < LA_MIN) v = LA_MIN;
+    auto load_chunk = [&](int p0) {
+        sy.load(p0, len);
+        sz.load(p0, len);
+        if (MODE != STATE) sx.load(p0, len);
+        if (MODE >= OUTU) sw.load(p0, len);
+        if (wave == 0) {  // the decay of each position
+            const int p = p0 + lane;
+            float v = 0.f;
+            if (lane < CT && p >= 0 && p < len) {
+                const int64_t tok = rev ? first - p + 1 : first + p;
+                if (tok < sg.end) v = a.la[a.la_tok ? tok * a.H + h : h];
+                if (v < LA_MIN) v = LA_MIN;
+            }
+            la_next = v;
         }
-        la_next = v;
     };
-    auto load_tiles = [&](int p) {
-        const int64_t base = first + static_cast<int64_t>(dir) * p;
-        const int cnt = len - p;
-        sy.template load<VEC>(a.y, base, dir, cnt, a.H, h, a.dx, 0, tid);
-        sz.template load<VEC>(a.z, base, dir, cnt, a.H, h, a.dz, col0, tid);
-        if (MODE != STATE) sx.template load<VEC>(a.x, base, dir, cnt, a.H, h, a.dx, 0, tid);
-        load_la(p);
-    };
-    load_tiles(0);
+    // this lane's outputs: NC neighbouring columns of token row 16 rt + ls
+    constexpr int NC = 4 * NT;
+    const int oc = col0 + wcol + NC * g;
+    const int64_t orow = static_cast<int64_t>(a.H) * a.dz;
+    T *obase = MODE != STATE ? static_cast<T *>(a.out) + (first * a.H + h) * a.dz : nullptr;
+    const int ooff = oc < a.dz ? ((rev ? 15 - ls : ls) * static_cast<int>(orow) + oc) * ESZ : NOWHERE;
 
-    for (int p0 = 0; p0 < len; p0 += CT) {
+    // chunks keep the forward order's borders: in reverse the ragged one is first
+    const int begin = rev ? -((CT - len % CT) % CT) : 0;
+    if (len > 0) load_chunk(begin);
+
+    for (int p0 = begin; p0 < len; p0 += CT) {
         __syncthreads();  // the previous chunk's readers
         sy.store(s_y, tid);
         sz.store(s_z, tid);
         if (MODE != STATE) sx.store(s_x, tid);
+        if (MODE >= OUTU) sw.store(s_w, tid);
         if (wave == 0) {
             // running sums in 64 bits: a far reset must not cost the decays
             // that follow it their low bits
-            double v = static_cast<double>(la_next) * LOG2E;
-#pragma unroll
-            for (int o = 1; o < CT; o <<= 1) {
-                const double up = __shfl_up(v, o);
-                if (lane >= o) v += up;
-            }
-            const double all = __shfl(v, CT - 1);
+            const double v = wave_prefix(static_cast<double>(la_next) * LOG2E);
+            const double all = last_lane(v);
             if (lane < CT) {
                 s_g[lane] = v;
                 s_e[lane] = a.s_scale * __builtin_amdgcn_exp2f(static_cast<float>(v));
                 s_f[lane] = a.u_scale * __builtin_amdgcn_exp2f(static_cast<float>(all - v));
-                if (lane == 0) *s_gam = __builtin_amdgcn_exp2f(static_cast<float>(all));
             }
+            if (lane == 0) *s_gam = __builtin_amdgcn_exp2f(static_cast<float>(all));
             total += all;
         }
         __syncthreads();
-        if (p0 + CT < len) load_tiles(p0 + CT);
+        if (p0 + CT < len) load_chunk(p0 + CT);
 
         Frag zf[KT][NT];
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int p = lane & 3;
-                if (NT == 2)
-                    zf[kt][t] = TZ::col_frag(s_z, kt, (wcol >> 3) + p, t, lane);
-                else if (sizeof(T) == 2)
-                    zf[kt][t] = TZ::col_frag(s_z, kt, (wcol >> 3) + (p >> 1), p & 1, lane);
-                else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        zf[kt][t][e] = reinterpret_cast<const float *>(s_z + (32 * kt + 8 * g + e) * TZ::BYTES)[wcol + ls];
-                }
+                if constexpr (NT == 2)
+                    zf[kt][t] = TZ::col_frag(s_z, kt, (wcol >> 3) + (lane & 3), t, lane);
+                else if constexpr (ESZ == 2)
+                    zf[kt][t] = TZ::col_frag(s_z, kt, (wcol >> 3) + ((lane >> 1) & 1), lane & 1, lane);
+                else
+                    zf[kt][t] = TZ::column(s_z, kt, wcol + ls, lane);
             }
 
-        if (MODE != STATE) {
+        if constexpr (MODE != STATE) {
             // scores, transposed (rows j, columns i), so that a lane holds
-            // four neighbouring j of one i
+            // four neighbouring j of one i; 16 x 16 tiles on and below the diagonal
             constexpr int TILES = RT * (RT + 1) / 2;
             for (int n = wave; n < TILES; n += NW) {
-                int it = 0, jt = n;
-                while (jt > it) {
-                    ++it;
-                    jt -= it;
-                }
+                const int it = static_cast<int>((0x3333222110ull >> (4 * n)) & 15);
+                const int jt = static_cast<int>((0x3210210100ull >> (4 * n)) & 15);
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    acc = E::mma(TX::row_frag(s_y, 16 * jt + ls, 4 * ks + g), TX::row_frag(s_x, 16 * it + ls, 4 * ks + g), acc);
+                    acc = E::mma(TX::row_frag(s_y + 16 * jt * TX::BYTES, ls, 4 * ks + g),
+                                 TX::row_frag(s_x + 16 * it * TX::BYTES, ls, 4 * ks + g), acc);
                 const int i = 16 * it + ls, j = 16 * jt + 4 * g;
                 const double gi = s_g[i];
-                float pr[4];
+                f32x4 pr;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    pr[r] = j + r <= i ? acc[r] * (a.p_scale * __builtin_amdgcn_exp2f(static_cast<float>(gi - s_g[j + r])))
-                                       : 0.f;
-                if (sizeof(T) == 2) {
-                    float rest[4] = {pr[0], pr[1], pr[2], pr[3]};
+                for (int r = 0; r < 4; ++r) {
+                    const float d = a.p_scale * __builtin_amdgcn_exp2f(static_cast<float>(gi - s_g[j + r]));
+                    pr[r] = j + r <= i ? acc[r] * d : 0.f;
+                }
+                if constexpr (ESZ == 2) {
+                    f32x4 rest = pr;
+                    const int at = Sc::at(jt >> 1, i, 2 * (jt & 1) + (g >> 1)) + 8 * (g & 1);
 #pragma unroll
                     for (int q = 0; q < NP; ++q) {
                         const bf16x2 lo = __builtin_convertvector((f32x2{rest[0], rest[1]}), bf16x2);
                         const bf16x2 hi = __builtin_convertvector((f32x2{rest[2], rest[3]}), bf16x2);
                         const uint2 w = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-                        *reinterpret_cast<uint2 *>(s_p + q * Sh::PB + TP::unit(i, j >> 3) + 8 * (g & 1)) = w;
+                        *reinterpret_cast<uint2 *>(s_p + q * Sc::BYTES + at) = w;
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             rest[r] -= static_cast<float>(lo[r]);
@@ -432,7 +574,25 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
                         }
                     }
                 } else {
-                    *reinterpret_cast<f32x4 *>(s_p + TP::unit(i, j >> 2)) = f32x4{pr[0], pr[1], pr[2], pr[3]};
+                    *reinterpret_cast<f32x4 *>(s_p + Sc::at(0, i, j >> 2)) = pr;
+                }
+                if constexpr (MODE == OUTM) {
+                    f32x4 m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < Sh::WC / 32; ++ks)
+                        m = E::mma(TZ::row_frag(s_z + 16 * jt * TZ::BYTES, ls, 4 * ks + g),
+                                   TZ::row_frag(s_w + 16 * it * TZ::BYTES, ls, 4 * ks + g), m);
+                    float rs = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        m[r] = j + r < i ? m[r] * pr[r] : 0.f;
+                        rs += m[r];
+                        m[r] = row16_sum(m[r]);
+                    }
+                    rs += __shfl_xor(rs, 16);
+                    rs += __shfl_xor(rs, 32);
+                    if (g == 0) s_m[(it * (RT + 1) + jt) * 16 + ls] = rs;
+                    if (ls == 15) *reinterpret_cast<f32x4 *>(s_m + (jt * (RT + 1) + it + 1) * 16 + 4 * g) = m;
                 }
             }
 
@@ -454,7 +614,7 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const Frag xf = TX::row_frag(s_x, 16 * rt + ls, 4 * ks + g);
+                    const Frag xf = TX::row_frag(s_x + 16 * rt * TX::BYTES, ls, 4 * ks + g);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -466,8 +626,37 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
                 const float e = s_e[16 * rt + ls];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) O[rt][t] *= e;
+                if constexpr (MODE >= OUTU) {
+                    float us = 0.f;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const f32x4 w = TZ::quad(s_w + 16 * rt * TZ::BYTES, ls, (wcol >> 2) + NT * g + t);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) us += O[rt][t][r] * w[r];
+                    }
+                    us += __shfl_xor(us, 16);
+                    us += __shfl_xor(us, 32);
+                    if (g == 0) s_u[wave * CT + 16 * rt + ls] = us;
+                }
             }
             __syncthreads();  // the scores
+            if constexpr (MODE >= OUTU) {
+                const int p = p0 + tid;
+                if (tid < CT && p >= 0 && p < len) {
+                    float us = 0.f;
+#pragma unroll
+                    for (int q = 0; q < NW; ++q) us += s_u[q * CT + tid];
+                    if constexpr (MODE == OUTM) {
+                        const int blk = tid >> 4;
+#pragma unroll
+                        for (int q = 0; q <= RT; ++q) {
+                            const float v = s_m[(blk * (RT + 1) + q) * 16 + (tid & 15)];
+                            us += q <= blk ? v : -v;
+                        }
+                    }
+                    a.u[static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p)] = us;
+                }
+            }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -475,58 +664,48 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
                     if (32 * kt <= 16 * rt + 15) {
 #pragma unroll
                         for (int q = 0; q < NP; ++q) {
-                            const Frag pf = TP::row_frag(s_p + q * Sh::PB, 16 * rt + ls, 4 * kt + g);
+                            const Frag pf = Sc::frag(s_p + q * Sc::BYTES + 16 * rt * Sc::ROW, kt, ls, g);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) O[rt][t] = E::mma(zf[kt][t], pf, O[rt][t]);
                         }
                     }
-            // a lane's columns: NT = 2: 8g .. 8g+7 of the wave's, NT = 1: 4g .. 4g+3
-            constexpr int NC = 4 * NT;
-            const int c = col0 + wcol + NC * g;
+            {
+                T *o = obase + (rev ? -(p0 + CT - 1) : p0) * orow;
+                const bool full = p0 >= 0 && p0 + CT <= len;
+                if constexpr (VEC) {
+                    const auto b = buffer(o);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const int i = 16 * rt + ls;
-                float v[NC], us = 0.f;
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const int p = p0 + 16 * rt + ls;
+                        const int off = full || (p >= 0 && p < len) ? ooff : NOWHERE;
+                        const int add = 16 * (rev ? RT - 1 - rt : rt) * static_cast<int>(orow) * ESZ;
+                        if constexpr (ESZ == 2) {
+                            uint32_t w[2 * NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[4 * t + r] = O[rt][t][r];
-                if (p0 + i < len && c < a.dz) {
-                    const int64_t at = ((first + static_cast<int64_t>(dir) * (p0 + i)) * a.H + h) * a.dz + c;
-                    T *o = static_cast<T *>(a.out) + at;
-                    if (VEC) {
-                        typedef T Tv __attribute__((ext_vector_type(4)));
-#pragma unroll
-                        for (int q = 0; q < NC; q += 4)
-                            if (NC == 4 || sizeof(T) == 2 || c + q < a.dz) {
-                                const f32x4 f = {v[q], v[q + 1], v[q + 2], v[q + 3]};
-                                *reinterpret_cast<Tv *>(o + q) = __builtin_convertvector(f, Tv);
+                            for (int t = 0; t < NT; ++t) {
+                                w[2 * t] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{O[rt][t][0], O[rt][t][1]}), bf16x2));
+                                w[2 * t + 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{O[rt][t][2], O[rt][t][3]}), bf16x2));
                             }
-                    } else {
+                            if constexpr (NT == 2)
+                                __builtin_amdgcn_raw_buffer_store_b128((u32x4{w[0], w[1], w[2], w[3]}), b, off, add, 0);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[1]}), b, off, add, 0);
+                        } else {
 #pragma unroll
-                        for (int q = 0; q < NC; ++q)
-                            if (c + q < a.dz) o[q] = static_cast<T>(v[q]);
+                            for (int t = 0; t < NT; ++t)
+                                if (t == 0 || oc + 4 < a.dz)
+                                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[rt][t]), b, off, add + 16 * t, 0);
+                        }
                     }
-                    if (MODE == OUTU) {
-                        const T *w = static_cast<const T *>(a.w) + at;
+                } else {
 #pragma unroll
-                        for (int q = 0; q < NC; ++q)
-                            if (c + q < a.dz) us += v[q] * static_cast<float>(w[q]);
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const int i = 16 * rt + ls, p = p0 + i;
+                        if (p >= 0 && p < len)
+#pragma unroll
+                            for (int q = 0; q < NC; ++q)
+                                if (oc + q < a.dz) o[(rev ? CT - 1 - i : i) * orow + oc + q] = static_cast<T>(O[rt][q >> 2][q & 3]);
                     }
-                }
-                if (MODE == OUTU) {
-                    us += __shfl_xor(us, 16);
-                    us += __shfl_xor(us, 32);
-                    if (g == 0) s_u[wave * CT + i] = us;
-                }
-            }
-            if (MODE == OUTU) {
-                __syncthreads();
-                if (tid < CT && p0 + tid < len) {
-                    float us = 0.f;
-#pragma unroll
-                    for (int q = 0; q < NW; ++q) us += s_u[q * CT + tid];
-                    a.u[(static_cast<int64_t>(cb) * a.H + h) * a.tokens + first + static_cast<int64_t>(dir) * (p0 + tid)] = us;
                 }
             }
         }
@@ -540,14 +719,13 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             Frag zu[NT][NU];
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = s_f[32 * kt + 8 * g + e];
+            const f32x4 f0 = *reinterpret_cast<const f32x4 *>(s_f + 32 * kt + 8 * g);
+            const f32x4 f1 = *reinterpret_cast<const f32x4 *>(s_f + 32 * kt + 8 * g + 4);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = f[e] * E::at(zf[kt][t], e);
+                for (int e = 0; e < 8; ++e) v[e] = (e < 4 ? f0[e & 3] : f1[e & 3]) * E::at(zf[kt][t], e);
                 E::template split<NU>(v, zu[t]);
             }
 #pragma unroll
@@ -564,17 +742,17 @@ __device__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
     if (a.s_out) {
         // in reverse order the state has yet to pass the first token's decay
         float fin = 1.f;
-        if (MODE != STATE && a.rev && len > 0) fin = __expf(a.la[a.la_tok ? sg.lo * a.H + h : h]);
+        if (MODE != STATE && rev && len > 0) fin = __expf(a.la[a.la_tok ? sg.lo * a.H + h : h]);
+        const auto b = buffer(a.s_out + sh * dkv, 4 * dkv);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int ch = 32 * (m >> 1) + 8 * g + 4 * (m & 1), col = col0 + wcol + zcol(t, ls);
-                float *p = a.s_out + sh * dkv;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (ch + r < a.dx && col < a.dz) p[static_cast<int64_t>(ch + r) * a.dz + col] = fin * S[m][t][r];
-            }
+                for (int r = 0; r < 4; ++r) {
+                    const int ch = 32 * (m >> 1) + 4 * (m & 1) + r;
+                    store4(fin * S[m][t][r], b, all_ch || ch + 8 * g < a.dx ? soff[t] : NOWHERE, 4 * ch * a.dz);
+                }
     }
     if (MODE == STATE && a.tot && cb == 0 && tid == 0) a.tot[sh] = total;
 }
@@ -590,7 +768,7 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t segheads, int ncb
 __host__ int64_t xcd_blocks(int64_t segheads, int ncb) { return (segheads + 7) / 8 * 8 * ncb; }
 
 template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU, bool VEC>
-__global__ void __launch_bounds__(64 * NW) sweep_kernel(SweepArgs a) {
+__global__ void __launch_bounds__(64 * NW, 2) sweep_kernel(SweepArgs a) {
     extern __shared__ __align__(16) char smem[];
     const int64_t item = xcd_item(blockIdx.x, a.segs * a.H, a.ncb);
     if (item < 0) return;
@@ -637,7 +815,7 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(ScanArgs a) {
 // d la of a segment: its last token's <S, dS>, then back over the segment the
 // differences of the row products, in 64 bits.  One wave per (segment, head).
 struct DecayArgs {
-    const float *uq, *uk;   // [ncb][H][tokens]
+    const float *uq, *uk;   // [H][tokens]
     const float *s_tab, *d_tab;  // states entering the segments, forward and reverse
     const float *s_fin;     // [N][H][dk*dv] final states
     const float *la;
@@ -646,7 +824,7 @@ struct DecayArgs {
     const int2 *tab, *seq;
     const int *pfx;
     int64_t N, T, tokens, segs, dkv;
-    int H, nseg, L, la_tok, nq, nk;
+    int H, nseg, L, la_tok;
 };
 
 __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs a) {
@@ -693,8 +871,8 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs a) {
         const int64_t t = top - 1 - lane;
         double v = 0.0;
         if (t >= lo) {
-            for (int c = 0; c < a.nq; ++c) v += a.uq[(static_cast<int64_t>(c) * a.H + h) * a.tokens + t];
-            for (int c = 0; c < a.nk; ++c) v -= a.uk[(static_cast<int64_t>(c) * a.H + h) * a.tokens + t];
+            const int64_t at = static_cast<int64_t>(h) * a.tokens + t;
+            v = static_cast<double>(a.uq[at]) - static_cast<double>(a.uk[at]);
         }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -888,8 +1066,8 @@ BwdSpace bwd_space(const LinArgs &a, const Cut &c, void *ws) {
     f.s_tot = b.take<double>(c.segs * a.H);
     f.d_tot = b.take<double>(c.segs * a.H);
     f.part = b.take<double>(c.segs * a.H);
-    f.uq = b.take<float>((a.dk + 63) / 64 * a.H * tokens);
-    f.uk = b.take<float>((a.dk + 63) / 64 * a.H * tokens);
+    f.uq = b.take<float>(a.H * tokens);
+    f.uk = b.take<float>(a.H * tokens);
     if (a.cu) f.plan = b.take<char>(static_cast<int64_t>(varlen_plan_bytes(a.N, a.T, c.L)));
     f.bytes = b.used;
     return f;
@@ -963,24 +1141,23 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     a.out = l.dq; a.w = l.q; a.u = f.uq;
     a.s_in = f.s_tab; a.s_t = 1;
     a.p_scale = a.s_scale = l.scale;
-    if ((e = launch_typed<OUTU, 3, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<OUTM, 2, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
     // dk
     a.x = l.v; a.y = l.d_o; a.z = l.q;
     a.out = l.dk_out; a.w = l.k; a.u = f.uk;
     a.s_in = f.d_tab; a.rev = 1;
     a.p_scale = a.u_scale = l.scale;
     a.s_scale = 1.f;
-    if ((e = launch_typed<OUTU, 3, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<OUTU, 2, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
     // dv
     a.x = l.k; a.y = l.q; a.z = l.d_o; a.dx = dk; a.dz = dv;
     a.out = l.dv_out; a.w = nullptr; a.u = nullptr;
     a.s_t = 0;
     if ((e = launch_typed<OUT, 2, 1, 2>(l, a, vec, s)) != hipSuccess) return e;
 
-    const int ncb = (dk + columns_of(dk) - 1) / columns_of(dk);
     DecayArgs d = {f.uq, f.uk, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,
                    l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,
-                   base.nseg, c.L, l.la_tok, ncb, ncb};
+                   base.nseg, c.L, l.la_tok};
     if (c.segs * l.H > 0) {
         hipLaunchKernelGGL(decay_grad_kernel, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(256), 0, s, d);
         if ((e = hipGetLastError()) != hipSuccess) return e;
