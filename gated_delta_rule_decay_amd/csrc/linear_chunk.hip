@@ -25,6 +25,8 @@
 // Long sequences are cut into segments: a state-only sweep forms what every
 // segment adds to the state, a scan over the segments turns these into the
 // state that enters each, and the sweeps then run over all segments at once.
+#include <initializer_list>
+
 #include "kernels.h"
 #include "linear.h"
 
@@ -259,6 +261,8 @@ __device__ __forceinline__ void store4(float v, __amdgpu_buffer_rsrc_t b, int of
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b, off, add, 0);
 }
 
+__device__ __forceinline__ bool inside(int p, int len) { return static_cast<unsigned>(p) < static_cast<unsigned>(len); }
+
 // Rows of one tensor for the chunks of a segment, staged in registers: CT
 // rows of COLS columns, thread by thread in 16-byte units.  Positions run
 // forward from token `first`, or (rev) back from it.
@@ -266,42 +270,41 @@ template <class T, int COLS, int CT, int NTH, bool VEC>
 struct Stage {
     using Tl = Tile<T, COLS>;
     static constexpr int RX = NTH / Tl::UNITS, N = CT / RX;  // rows of a pass, passes
-    static_assert(RX <= CT && CT % RX == 0 && (sizeof(T) == 4 || RX % 16 == 0), "whole passes, of one permutation");
+    static_assert(RX <= CT && CT % RX == 0, "whole passes");
     u32x4 r[N];
-    const T *base;  // row of position 0, column 0 of the head
-    int64_t row;    // elements from one token to the next
+    const T *base;  // row of position 0 (rev: of position -(CT-1)), column 0 of the head
+    int64_t row;    // elements from one position to the next
     int off;        // this thread's bytes in pass 0 (rev: in the last)
+    int add0, step; // bytes of pass 0, from pass to pass
     int r0, c, d;
-    bool rev;
 
-    __device__ __forceinline__ void init(const void *p, int64_t first, int64_t H, int h, int d_, int col0, bool rev_, int tid) {
+    __device__ __forceinline__ void init(const void *p, int64_t first, int H, int h, int d_, int col0, bool rev, int tid) {
         d = d_;
-        rev = rev_;
-        row = H * d;
+        const int pitch = H * d;
+        row = rev ? -static_cast<int64_t>(pitch) : pitch;
         base = static_cast<const T *>(p) + (first * H + h) * d;
         r0 = tid / Tl::UNITS;
         c = col0 + (tid % Tl::UNITS) * Tl::PER;
-        const int at = rev ? RX - 1 - r0 : r0;
-        off = c < d ? (at * static_cast<int>(row) + c) * static_cast<int>(sizeof(T)) : NOWHERE;
+        if (VEC) {
+            if (rev) base -= static_cast<int64_t>(CT - 1) * pitch;
+            off = c < d ? ((rev ? RX - 1 - r0 : r0) * pitch + c) * static_cast<int>(sizeof(T)) : NOWHERE;
+            step = (rev ? -RX : RX) * pitch * static_cast<int>(sizeof(T));
+            add0 = rev ? -(N - 1) * step : 0;
+        }
     }
     // positions p0 .. p0+CT-1, of which [0, len) exist
     __device__ __forceinline__ void load(int p0, int len) {
         if (VEC) {
-            const auto b = buffer(base + (rev ? -(p0 + CT - 1) : p0) * row);
-            const bool full = p0 >= 0 && p0 + CT <= len;
+            const auto b = buffer(base + p0 * row);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int p = p0 + r0 + i * RX;
-                r[i] = load16(b, full || (p >= 0 && p < len) ? off : NOWHERE,
-                              (rev ? N - 1 - i : i) * RX * static_cast<int>(row) * static_cast<int>(sizeof(T)));
-            }
+            for (int i = 0; i < N; ++i) r[i] = load16(b, inside(p0 + r0 + i * RX, len) ? off : NOWHERE, add0 + i * step);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int p = p0 + r0 + i * RX;
                 u32x4 v = {0, 0, 0, 0};
-                if (p >= 0 && p < len && c < d) {
-                    const T *s = base + (rev ? -p : p) * row + c;
+                if (inside(p, len) && c < d) {
+                    const T *s = base + p * row + c;
                     if (sizeof(T) == 2) {
                         const uint16_t *e = reinterpret_cast<const uint16_t *>(s);
 #pragma unroll
@@ -319,9 +322,8 @@ struct Stage {
         }
     }
     __device__ __forceinline__ void store(char *t, int tid) const {
-        const int at = Tl::unit(r0, tid % Tl::UNITS);
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(t + at + i * RX * Tl::BYTES) = r[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(t + Tl::unit(r0 + i * RX, tid % Tl::UNITS)) = r[i];
     }
 };
 
@@ -361,15 +363,16 @@ constexpr int OUT = 1;    // outputs (and the state)
 constexpr int OUTU = 2;   // outputs and u, the read's row products <w, x S>
 constexpr int OUTM = 3;   // OUTU, and in u what the pairs inside a chunk add
 
-template <class T, int DX, int NW, int NT>
+template <class T, int DX, int NC, int NT, int KSP>
 struct Shape {
-    static constexpr int CT = Elem<T>::CT, WC = NW * 16 * NT;  // columns of a workgroup
+    static constexpr int CT = Elem<T>::CT, NW = NC * KSP, WC = NC * 16 * NT;  // columns of a workgroup
     using TX = Tile<T, DX>;
     using TZ = Tile<T, WC>;
     static constexpr int XB = CT * TX::BYTES, ZB = CT * TZ::BYTES;
+    static constexpr int OB = KSP > 1 ? NW * (CT / 32) * NT * 1024 : 0;  // read sums passed between waves
     static constexpr size_t bytes(int mode, int np) {
         return CT * 8 + 2 * CT * 4 + 16 + (mode == STATE ? 1 : 2) * XB + (mode >= OUTU ? 2 : 1) * ZB +
-               (mode == STATE ? 0 : np * Scores<T>::BYTES) + (mode >= OUTU ? NW * CT * 4 : 0) +
+               (mode == STATE ? 0 : np * Scores<T>::BYTES + OB) + (mode >= OUTU ? NW * CT * 4 : 0) +
                (mode == OUTM ? (CT / 16 + 1) * CT * 4 : 0);
     }
 };
@@ -391,19 +394,22 @@ struct Shape {
 //   M_ij = (score i, j) (w_i . z_j):
 // pairs inside a chunk enter both their ends with the same fp32 value, so the
 // sum over a chunk's tail keeps their precision.
-template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU, bool VEC>
+template <class T, int DX, int NCW, int NT, int KSP, int MODE, int NP, int NS, int NU, bool VEC>
 __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
     using E = Elem<T>;
     using Frag = typename E::Frag;
-    using Sh = Shape<T, DX, NW, NT>;
+    using Sh = Shape<T, DX, NCW, NT, KSP>;
     using TX = typename Sh::TX;
     using TZ = typename Sh::TZ;
     using Sc = Scores<T>;
-    constexpr int CT = E::CT, KT = CT / 32, RT = CT / 16, KS = DX / 32, MT = DX / 16, NTH = 64 * NW;
-    constexpr int ESZ = sizeof(T);
+    constexpr int CT = E::CT, NW = Sh::NW, NTH = 64 * NW, ESZ = sizeof(T);
+    constexpr int KT = CT / 32, RT = CT / 16, KS = DX / 32;     // blocks of tokens, row tiles, blocks of channels
+    constexpr int KSW = KS / KSP, MT = 2 * KSW, RTW = RT / KSP;  // a wave's blocks, state tiles, row tiles
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, ls = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kp = KSP > 1 ? wave / NCW : 0, cw = KSP > 1 ? wave % NCW : wave;  // the wave's channels and columns
+    const int ch0 = 32 * KSW * kp;
     const int cb = static_cast<int>(item % a.ncb);
     const int64_t sh = item / a.ncb;  // segment * H + head
     const int64_t seg = sh / a.H;
@@ -411,7 +417,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     if (a.nsegs && seg >= *a.nsegs) return;
     const Seg sg = segment(a, seg);
     const int len = __builtin_amdgcn_readfirstlane(static_cast<int>(sg.hi - sg.lo));
-    const int col0 = cb * Sh::WC, wcol = 16 * NT * wave;  // first column of the workgroup, of the wave in it
+    const int col0 = cb * Sh::WC, wcol = 16 * NT * cw;  // first column of the workgroup, of the wave in it
     const bool rev = a.rev;
     const int64_t first = rev ? sg.hi - 1 : sg.lo;  // token of position 0
 
@@ -425,7 +431,9 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     char *s_p = s_x + Sh::XB;
     char *s_w = s_p + NP * Sc::BYTES;
     float *s_u = reinterpret_cast<float *>(s_w + Sh::ZB);  // [NW][CT]
-    float *s_m = s_u + NW * CT;  // [CT/16 blocks][CT/16 + 1][16]: row sums of the block's tiles, then column sums
+    float *s_m = s_u + (MODE >= OUTU ? NW * CT : 0);  // [CT/16 blocks][CT/16 + 1][16]: row sums of the block's tiles, then column sums
+
+    float *s_o = MODE >= OUTU ? s_m + (MODE == OUTM ? (RT + 1) * CT : 0) : reinterpret_cast<float *>(s_w);  // [NW][RTW][NT][64 lanes][4]
 
     // column of slot s of tile t, relative to the wave's
     auto zcol = [](int t, int s) { return NT == 2 ? 8 * (s >> 2) + 4 * t + (s & 3) : s; };
@@ -442,7 +450,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int col = col0 + wcol + zcol(t, ls);
-        soff[t] = col < a.dz ? 4 * (8 * g * a.dz + col) : NOWHERE;
+        soff[t] = col < a.dz ? 4 * ((ch0 + 8 * g) * a.dz + col) : NOWHERE;
     }
     if (MODE != STATE && a.s_in) {
         const auto b = buffer(a.s_in + sh * dkv, 4 * dkv);
@@ -454,17 +462,23 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                 if (!a.s_t) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        S[m][t][r] = load4(b, all_ch || ch + 8 * g + r < a.dx ? soff[t] : NOWHERE, 4 * (ch + r) * a.dz);
+                        S[m][t][r] = load4(b, all_ch || ch0 + ch + 8 * g + r < a.dx ? soff[t] : NOWHERE, 4 * (ch + r) * a.dz);
                 } else {
                     const int col = col0 + wcol + zcol(t, ls);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int c = ch + 8 * g + r;
+                        const int c = ch0 + ch + 8 * g + r;
                         S[m][t][r] = load4(b, c < a.dx && col < a.dz ? 4 * (col * a.dx + c) : NOWHERE, 0);
                     }
                 }
             }
     }
+    // the state is waited for here: a wait inside the chunk loop would also
+    // wait for the next chunk's rows
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(S[m][t]));
     if (MODE != STATE)  // the score tiles above the diagonal stay zero
         for (int i = tid; i < NP * Sc::BYTES / 4; i += NTH) reinterpret_cast<uint32_t *>(s_p)[i] = 0;
 
@@ -474,22 +488,40 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     sz.init(a.z, first, a.H, h, a.dz, col0, rev, tid);
     if (MODE != STATE) sx.init(a.x, first, a.H, h, a.dx, 0, rev, tid);
     if (MODE >= OUTU) sw.init(a.w, first, a.H, h, a.dz, col0, rev, tid);
-    double total = 0.0;  // log2 decays before this chunk (wave 0)
+    double total = 0.0;  // log2 decays of the staged chunks (last wave)
     float la_next = 0.f;
+    // position p takes the decay of token first + p, or (rev) first - p + 1,
+    // the token behind it: none for the sequence's last token
+    const int64_t la_pitch = a.la_tok ? a.H : 0, la_row = rev ? -la_pitch : la_pitch;
+    const float *la_base = a.la + h + (rev ? first + 1 - (CT - 1) : first) * la_pitch;
+    const int la_off = static_cast<int>(rev ? CT - 1 - lane : lane) * static_cast<int>(la_pitch) * 4;
+    const int la_skip = rev && sg.hi == sg.end ? -1 : 0;  // position 0 has none
     auto load_chunk = [&](int p0) {
         sy.load(p0, len);
         sz.load(p0, len);
         if (MODE != STATE) sx.load(p0, len);
         if (MODE >= OUTU) sw.load(p0, len);
-        if (wave == 0) {  // the decay of each position
-            const int p = p0 + lane;
-            float v = 0.f;
-            if (lane < CT && p >= 0 && p < len) {
-                const int64_t tok = rev ? first - p + 1 : first + p;
-                if (tok < sg.end) v = a.la[a.la_tok ? tok * a.H + h : h];
-                if (v < LA_MIN) v = LA_MIN;
+        if (wave == NW - 1)  // the decay of each position
+            la_next = load4(buffer(la_base + p0 * la_row), inside(p0 + lane + la_skip, len + la_skip) && lane < CT ? la_off : NOWHERE, 0);
+    };
+    // the loaded chunk into LDS, its decays summed
+    auto stage_chunk = [&] {
+        sy.store(s_y, tid);
+        sz.store(s_z, tid);
+        if (MODE != STATE) sx.store(s_x, tid);
+        if (MODE >= OUTU) sw.store(s_w, tid);
+        if (wave == NW - 1) {
+            // running sums in 64 bits: a far reset must not cost the decays
+            // that follow it their low bits
+            const double v = wave_prefix(static_cast<double>(la_next < LA_MIN ? LA_MIN : la_next) * LOG2E);
+            const double all = last_lane(v);
+            if (lane < CT) {
+                s_g[lane] = v;
+                s_e[lane] = a.s_scale * __builtin_amdgcn_exp2f(static_cast<float>(v));
+                s_f[lane] = a.u_scale * __builtin_amdgcn_exp2f(static_cast<float>(all - v));
             }
-            la_next = v;
+            if (lane == 0) *s_gam = __builtin_amdgcn_exp2f(static_cast<float>(all));
+            total += all;
         }
     };
     // this lane's outputs: NC neighbouring columns of token row 16 rt + ls
@@ -501,28 +533,13 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 
     // chunks keep the forward order's borders: in reverse the ragged one is first
     const int begin = rev ? -((CT - len % CT) % CT) : 0;
-    if (len > 0) load_chunk(begin);
+    if (len > 0) {
+        load_chunk(begin);
+        stage_chunk();
+    }
+    __syncthreads();
 
     for (int p0 = begin; p0 < len; p0 += CT) {
-        __syncthreads();  // the previous chunk's readers
-        sy.store(s_y, tid);
-        sz.store(s_z, tid);
-        if (MODE != STATE) sx.store(s_x, tid);
-        if (MODE >= OUTU) sw.store(s_w, tid);
-        if (wave == 0) {
-            // running sums in 64 bits: a far reset must not cost the decays
-            // that follow it their low bits
-            const double v = wave_prefix(static_cast<double>(la_next) * LOG2E);
-            const double all = last_lane(v);
-            if (lane < CT) {
-                s_g[lane] = v;
-                s_e[lane] = a.s_scale * __builtin_amdgcn_exp2f(static_cast<float>(v));
-                s_f[lane] = a.u_scale * __builtin_amdgcn_exp2f(static_cast<float>(all - v));
-            }
-            if (lane == 0) *s_gam = __builtin_amdgcn_exp2f(static_cast<float>(all));
-            total += all;
-        }
-        __syncthreads();
         if (p0 + CT < len) load_chunk(p0 + CT);
 
         Frag zf[KT][NT];
@@ -538,25 +555,30 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                     zf[kt][t] = TZ::column(s_z, kt, wcol + ls, lane);
             }
 
+        f32x4 O[RT][NT];
         if constexpr (MODE != STATE) {
             // scores, transposed (rows j, columns i), so that a lane holds
             // four neighbouring j of one i; 16 x 16 tiles on and below the diagonal
-            constexpr int TILES = RT * (RT + 1) / 2;
-            for (int n = wave; n < TILES; n += NW) {
-                const int it = static_cast<int>((0x3333222110ull >> (4 * n)) & 15);
-                const int jt = static_cast<int>((0x3210210100ull >> (4 * n)) & 15);
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            // Surplus waves form the last tile again and write the same values.
+            constexpr int TILES = RT * (RT + 1) / 2, MINE = (TILES + NW - 1) / NW;
+            auto product = [&](int it, int jt) {
+                f32x4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    acc = E::mma(TX::row_frag(s_y + 16 * jt * TX::BYTES, ls, 4 * ks + g),
-                                 TX::row_frag(s_x + 16 * it * TX::BYTES, ls, 4 * ks + g), acc);
+                    sc = E::mma(TX::row_frag(s_y + 16 * jt * TX::BYTES, ls, 4 * ks + g),
+                                TX::row_frag(s_x + 16 * it * TX::BYTES, ls, 4 * ks + g), sc);
+                return sc;
+            };
+            auto finish = [&](int it, int jt, f32x4 sc) {
                 const int i = 16 * it + ls, j = 16 * jt + 4 * g;
                 const double gi = s_g[i];
                 f32x4 pr;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float d = a.p_scale * __builtin_amdgcn_exp2f(static_cast<float>(gi - s_g[j + r]));
-                    pr[r] = j + r <= i ? acc[r] * d : 0.f;
+                    float v = sc[r] * d;
+                    asm("" : "+v"(v));  // formed on every lane: a branch costs more
+                    pr[r] = j + r <= i ? v : 0.f;
                 }
                 if constexpr (ESZ == 2) {
                     f32x4 rest = pr;
@@ -594,16 +616,31 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                     if (g == 0) s_m[(it * (RT + 1) + jt) * 16 + ls] = rs;
                     if (ls == 15) *reinterpret_cast<f32x4 *>(s_m + (jt * (RT + 1) + it + 1) * 16 + 4 * g) = m;
                 }
+            };
+            auto tile_i = [&](int n) { return static_cast<int>((0x3333222110ull >> (4 * n)) & 15); };
+            auto tile_j = [&](int n) { return static_cast<int>((0x3210210100ull >> (4 * n)) & 15); };
+            if constexpr (KSP > 1) {  // one workgroup a CU: all at once, branch-free
+                f32x4 sc[MINE];
+                int n[MINE];
+#pragma unroll
+                for (int u = 0; u < MINE; ++u) {
+                    n[u] = min(wave + u * NW, TILES - 1);
+                    sc[u] = product(tile_i(n[u]), tile_j(n[u]));
+                }
+#pragma unroll
+                for (int u = 0; u < MINE; ++u) finish(tile_i(n[u]), tile_j(n[u]), sc[u]);
+            } else {  // two: one by one, in fewer registers
+#pragma unroll 1
+                for (int n = wave; n < TILES; n += NW) finish(tile_i(n), tile_j(n), product(tile_i(n), tile_j(n)));
             }
 
             // outputs, transposed: x S first, which needs no scores
-            f32x4 O[RT][NT];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) O[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
+            for (int ks = 0; ks < KSW; ++ks) {
                 Frag sf[NT][NS];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -614,7 +651,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const Frag xf = TX::row_frag(s_x + 16 * rt * TX::BYTES, ls, 4 * ks + g);
+                    const Frag xf = TX::row_frag(s_x + 16 * rt * TX::BYTES, ls, (ch0 >> 3) + 4 * ks + g);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -639,75 +676,13 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                     if (g == 0) s_u[wave * CT + 16 * rt + ls] = us;
                 }
             }
-            __syncthreads();  // the scores
-            if constexpr (MODE >= OUTU) {
-                const int p = p0 + tid;
-                if (tid < CT && p >= 0 && p < len) {
-                    float us = 0.f;
+            if constexpr (KSP > 1)  // the other half's row tiles go to the wave that finishes them
 #pragma unroll
-                    for (int q = 0; q < NW; ++q) us += s_u[q * CT + tid];
-                    if constexpr (MODE == OUTM) {
-                        const int blk = tid >> 4;
+                for (int rt = 0; rt < RT; ++rt)
+                    if (rt / RTW != kp)
 #pragma unroll
-                        for (int q = 0; q <= RT; ++q) {
-                            const float v = s_m[(blk * (RT + 1) + q) * 16 + (tid & 15)];
-                            us += q <= blk ? v : -v;
-                        }
-                    }
-                    a.u[static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p)] = us;
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-                    if (32 * kt <= 16 * rt + 15) {
-#pragma unroll
-                        for (int q = 0; q < NP; ++q) {
-                            const Frag pf = Sc::frag(s_p + q * Sc::BYTES + 16 * rt * Sc::ROW, kt, ls, g);
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) O[rt][t] = E::mma(zf[kt][t], pf, O[rt][t]);
-                        }
-                    }
-            {
-                T *o = obase + (rev ? -(p0 + CT - 1) : p0) * orow;
-                const bool full = p0 >= 0 && p0 + CT <= len;
-                if constexpr (VEC) {
-                    const auto b = buffer(o);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const int p = p0 + 16 * rt + ls;
-                        const int off = full || (p >= 0 && p < len) ? ooff : NOWHERE;
-                        const int add = 16 * (rev ? RT - 1 - rt : rt) * static_cast<int>(orow) * ESZ;
-                        if constexpr (ESZ == 2) {
-                            uint32_t w[2 * NT];
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                w[2 * t] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{O[rt][t][0], O[rt][t][1]}), bf16x2));
-                                w[2 * t + 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{O[rt][t][2], O[rt][t][3]}), bf16x2));
-                            }
-                            if constexpr (NT == 2)
-                                __builtin_amdgcn_raw_buffer_store_b128((u32x4{w[0], w[1], w[2], w[3]}), b, off, add, 0);
-                            else
-                                __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[1]}), b, off, add, 0);
-                        } else {
-#pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                if (t == 0 || oc + 4 < a.dz)
-                                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[rt][t]), b, off, add + 16 * t, 0);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const int i = 16 * rt + ls, p = p0 + i;
-                        if (p >= 0 && p < len)
-#pragma unroll
-                            for (int q = 0; q < NC; ++q)
-                                if (oc + q < a.dz) o[(rev ? CT - 1 - i : i) * orow + oc + q] = static_cast<T>(O[rt][q >> 2][q & 3]);
-                    }
-                }
-            }
+                        for (int t = 0; t < NT; ++t)
+                            *reinterpret_cast<f32x4 *>(s_o + (((wave * RTW + rt % RTW) * NT + t) * 64 + lane) * 4) = O[rt][t];
         }
 
         // the state: decayed, plus the chunk's products
@@ -729,14 +704,111 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                 E::template split<NU>(v, zu[t]);
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const Frag yf = TX::col_frag(s_y, kt, 4 * (m >> 1) + (lane & 3), m & 1, lane);
+            for (int m = 0; m < MT; m += 2) {  // two tiles at a time: independent products between dependent ones
+                const int un = (ch0 >> 3) + 4 * (m >> 1) + (lane & 3);
+                const Frag y0 = TX::col_frag(s_y, kt, un, 0, lane), y1 = TX::col_frag(s_y, kt, un, 1, lane);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int q = 0; q < NU; ++q)
 #pragma unroll
-                    for (int q = 0; q < NU; ++q) S[m][t] = E::mma(yf, zu[t][q], S[m][t]);
+                    for (int t = 0; t < NT; ++t) {
+                        S[m][t] = E::mma(y0, zu[t][q], S[m][t]);
+                        S[m + 1][t] = E::mma(y1, zu[t][q], S[m + 1][t]);
+                    }
             }
         }
+
+        __syncthreads();  // the scores are written, the tiles read
+        if (p0 + CT < len) stage_chunk();
+
+        if constexpr (MODE != STATE) {
+            if constexpr (MODE >= OUTU) {
+                const int p = p0 + tid;
+                if (tid < CT && inside(p, len)) {
+                    float us = 0.f;
+#pragma unroll
+                    for (int q = 0; q < NW; ++q) us += s_u[q * CT + tid];
+                    if constexpr (MODE == OUTM) {
+                        const int blk = tid >> 4;
+#pragma unroll
+                        for (int q = 0; q <= RT; ++q) {
+                            const float v = s_m[(blk * (RT + 1) + q) * 16 + (tid & 15)];
+                            us += q <= blk ? v : -v;
+                        }
+                    }
+                    a.u[static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p)] = us;
+                }
+            }
+            // a wave finishes RTW row tiles from rt0 on
+            const int rt0 = RTW * kp;
+            f32x4 R[RTW][NT];
+#pragma unroll
+            for (int q = 0; q < RTW; ++q)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (KSP > 1) {
+                        const int other = wave < NCW ? wave + NCW : wave - NCW;
+                        R[q][t] = (kp ? O[RTW + q][t] : O[q][t]) +
+                                  *reinterpret_cast<const f32x4 *>(s_o + (((other * RTW + q) * NT + t) * 64 + lane) * 4);
+                    } else {
+                        R[q][t] = O[q][t];
+                    }
+                }
+#pragma unroll
+            for (int q = 0; q < RTW; ++q)
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+                    if (KSP > 1 ? (kt == 0 || kp > 0) : 32 * kt <= 16 * q + 15) {
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) {
+                            const Frag pf = Sc::frag(s_p + n * Sc::BYTES + 16 * (rt0 + q) * Sc::ROW, kt, ls, g);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) R[q][t] = E::mma(zf[kt][t], pf, R[q][t]);
+                        }
+                    }
+            {
+                T *o = obase + (rev ? -(p0 + CT - 1) : p0) * orow;
+                if constexpr (VEC) {
+                    const auto b = buffer(o);
+#pragma unroll
+                    for (int q = 0; q < RTW; ++q) {
+                        const int p = p0 + 16 * (rt0 + q) + ls;
+                        // 16-byte stores with a register as their uniform offset
+                        // have written registers that the next instruction
+                        // overwrote: the whole offset goes into the lane's
+                        const int off = inside(p, len) && ooff != NOWHERE
+                                            ? ooff + 16 * (rev ? RT - 1 - rt0 - q : rt0 + q) * static_cast<int>(orow) * ESZ
+                                            : NOWHERE;
+                        if constexpr (ESZ == 2) {
+                            uint32_t w[2 * NT];
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                w[2 * t] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{R[q][t][0], R[q][t][1]}), bf16x2));
+                                w[2 * t + 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{R[q][t][2], R[q][t][3]}), bf16x2));
+                            }
+                            if constexpr (NT == 2)
+                                __builtin_amdgcn_raw_buffer_store_b128((u32x4{w[0], w[1], w[2], w[3]}), b, off, 0, 0);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[1]}), b, off, 0, 0);
+                        } else {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, R[q][t]), b,
+                                                                       t == 0 || oc + 4 < a.dz ? off + 16 * t : NOWHERE, 0, 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < RTW; ++q) {
+                        const int i = 16 * (rt0 + q) + ls, p = p0 + i;
+                        if (inside(p, len))
+#pragma unroll
+                            for (int n = 0; n < NC; ++n)
+                                if (oc + n < a.dz) o[(rev ? CT - 1 - i : i) * orow + oc + n] = static_cast<T>(R[q][n >> 2][n & 3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the next chunk is staged, the scores read
     }
 
     if (a.s_out) {
@@ -751,10 +823,10 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int ch = 32 * (m >> 1) + 4 * (m & 1) + r;
-                    store4(fin * S[m][t][r], b, all_ch || ch + 8 * g < a.dx ? soff[t] : NOWHERE, 4 * ch * a.dz);
+                    store4(fin * S[m][t][r], b, all_ch || ch0 + ch + 8 * g < a.dx ? soff[t] : NOWHERE, 4 * ch * a.dz);
                 }
     }
-    if (MODE == STATE && a.tot && cb == 0 && tid == 0) a.tot[sh] = total;
+    if (MODE == STATE && a.tot && cb == 0 && tid == NTH - 64) a.tot[sh] = total;
 }
 
 // Workgroups with neighbouring numbers run on different XCDs (eight, in
@@ -767,12 +839,12 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t segheads, int ncb
 }
 __host__ int64_t xcd_blocks(int64_t segheads, int ncb) { return (segheads + 7) / 8 * 8 * ncb; }
 
-template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU, bool VEC>
-__global__ void __launch_bounds__(64 * NW, 2) sweep_kernel(SweepArgs a) {
+template <class T, int DX, int NCW, int NT, int KSP, int MODE, int NP, int NS, int NU, bool VEC>
+__global__ void __launch_bounds__(64 * NCW * KSP, 2) sweep_kernel(SweepArgs a) {
     extern __shared__ __align__(16) char smem[];
     const int64_t item = xcd_item(blockIdx.x, a.segs * a.H, a.ncb);
     if (item < 0) return;
-    sweep_body<T, DX, NW, NT, MODE, NP, NS, NU, VEC>(a, item, smem);
+    sweep_body<T, DX, NCW, NT, KSP, MODE, NP, NS, NU, VEC>(a, item, smem);
 }
 
 // The scan over a sequence's segments: what each adds to the state becomes
@@ -924,29 +996,29 @@ Cut cut_of(const LinArgs &a, int64_t L) {
     return c;
 }
 
-// Forward: segments only where whole sequences leave the chip empty.
+// Forward: segments only where whole chains leave the chip empty.
 Cut fwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
-    if (a.T <= 256 || heads >= 256) return Cut{0, 1, a.N};
+    if (a.T <= 256 || heads >= 128) return Cut{0, 1, a.N};
     int64_t L = (a.T * heads / 512 + 63) / 64 * 64;
     if (L < 256) L = 256;
     if (!a.cu && L >= a.T) return Cut{0, 1, a.N};
     return cut_of(a, L);
 }
 
-// Backward: segments of at most 1024 tokens, which also bounds how far the
-// differences of the decay's gradient are summed.
+// Backward: always through the segments' states, at most 1024 tokens apart,
+// which bounds how far the differences of the decay's gradient are summed.
 Cut bwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
-    int64_t L = (a.T * heads / 512 + 63) / 64 * 64;
+    int64_t L = (a.T * heads / 256 + 63) / 64 * 64;
     if (L < 256) L = 256;
     if (L > 1024) L = 1024;
     return cut_of(a, L);
 }
 
-template <class T, int DX, int NW, int NT, int MODE, int NP, int NS, int NU>
+template <class T, int DX, int NCW, int NT, int KSP, int MODE, int NP, int NS, int NU>
 hipError_t launch_shape(SweepArgs a, bool vec, hipStream_t s) {
-    using Sh = Shape<T, DX, NW, NT>;
+    using Sh = Shape<T, DX, NCW, NT, KSP>;
     a.ncb = (a.dz + Sh::WC - 1) / Sh::WC;
     const int64_t blocks = xcd_blocks(a.segs * a.H, a.ncb);
     if (blocks <= 0) return hipSuccess;
@@ -959,29 +1031,43 @@ hipError_t launch_shape(SweepArgs a, bool vec, hipStream_t s) {
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
             if (e != hipSuccess) return e;
         }
-        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(64 * NW), lds, s, a);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(64 * Sh::NW), lds, s, a);
         return hipGetLastError();
     };
-    if (vec) return go(sweep_kernel<T, DX, NW, NT, MODE, NP, NS, NU, true>);
-    return go(sweep_kernel<T, DX, NW, NT, MODE, NP, NS, NU, false>);
+    if (vec) return go(sweep_kernel<T, DX, NCW, NT, KSP, MODE, NP, NS, NU, true>);
+    return go(sweep_kernel<T, DX, NCW, NT, KSP, MODE, NP, NS, NU, false>);
 }
 
-// Columns of a workgroup: 128 (four waves of 32) or 64 (four of 16).
-int columns_of(int64_t dz) { return dz > 64 ? 128 : 64; }
+// The sweep's shapes: columns of a workgroup and how its waves share them.
+//   WIDE   128 columns, four waves of 32, two workgroups a CU
+//   TALL   128 columns, eight waves of 16: fewer registers a wave, for the
+//          sweeps that hold more operands
+//   SPLIT  64 columns, four pairs of waves, each pair sharing 16 columns and
+//          taking half of the channels: eight waves on half of a head, where
+//          heads are too few to fill the chip with whole ones
+// and up to 64 columns four waves of 16.
+enum Form { WIDE, TALL, SPLIT };
+
+template <class T, int DX, int MODE, int NP, int NS, int NU>
+hipError_t launch_width(const SweepArgs &a, Form form, bool vec, hipStream_t s) {
+    if (a.dz <= 64 && form != SPLIT) return launch_shape<T, DX, 4, 1, 1, MODE, NP, NS, NU>(a, vec, s);
+    if constexpr (MODE == OUT) {
+        if (form == SPLIT) return launch_shape<T, DX, 4, 1, 2, MODE, NP, NS, NU>(a, vec, s);
+        if (form == WIDE) return launch_shape<T, DX, 4, 2, 1, MODE, NP, NS, NU>(a, vec, s);
+    }
+    return launch_shape<T, DX, 8, 1, 1, MODE, NP, NS, NU>(a, vec, s);
+}
 
 template <class T, int MODE, int NP, int NS, int NU>
-hipError_t launch_sweep(const SweepArgs &a, bool vec, hipStream_t s) {
-    if (a.dx > 64)
-        return columns_of(a.dz) == 128 ? launch_shape<T, 128, 4, 2, MODE, NP, NS, NU>(a, vec, s)
-                                       : launch_shape<T, 128, 4, 1, MODE, NP, NS, NU>(a, vec, s);
-    return columns_of(a.dz) == 128 ? launch_shape<T, 64, 4, 2, MODE, NP, NS, NU>(a, vec, s)
-                                   : launch_shape<T, 64, 4, 1, MODE, NP, NS, NU>(a, vec, s);
+hipError_t launch_sweep(const SweepArgs &a, Form form, bool vec, hipStream_t s) {
+    if (a.dx > 64) return launch_width<T, 128, MODE, NP, NS, NU>(a, form, vec, s);
+    return launch_width<T, 64, MODE, NP, NS, NU>(a, form, vec, s);
 }
 
 template <int MODE, int NP, int NS, int NU>
-hipError_t launch_typed(const LinArgs &l, const SweepArgs &a, bool vec, hipStream_t s) {
-    if (l.bf16) return launch_sweep<__bf16, MODE, NP, NS, NU>(a, vec, s);
-    return launch_sweep<float, MODE, 1, 1, 1>(a, vec, s);
+hipError_t launch_typed(const LinArgs &l, const SweepArgs &a, Form form, bool vec, hipStream_t s) {
+    if (l.bf16) return launch_sweep<__bf16, MODE, NP, NS, NU>(a, form, vec, s);
+    return launch_sweep<float, MODE, 1, 1, 1>(a, form, vec, s);
 }
 
 SweepArgs sweep_of(const LinArgs &l, const Cut &c, const VarPlan *vp) {
@@ -1100,7 +1186,7 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
         st.s_in = nullptr;
         st.s_out = f.tab;
         st.tot = f.tot;
-        if ((e = launch_typed<STATE, 1, 1, 3>(l, st, vec, s)) != hipSuccess) return e;
+        if ((e = launch_typed<STATE, 1, 1, 3>(l, st, TALL, vec, s)) != hipSuccess) return e;
         ScanArgs sc = {f.tab, f.tot, l.s0, l.s_out, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
                        l.dk * l.dv, a.H, a.nseg, 0, l.la_tok, 0};
         if ((e = launch_scan(sc, s)) != hipSuccess) return e;
@@ -1108,7 +1194,9 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
         a.s_out = nullptr;
     }
     a.p_scale = a.s_scale = l.scale;
-    return launch_typed<OUT, 2, 1, 3>(l, a, vec, s);
+    // whole chains also give the final state: their updates keep 24 bits
+    if (cut) return launch_typed<OUT, 2, 1, 2>(l, a, WIDE, vec, s);
+    return launch_typed<OUT, 2, 1, 3>(l, a, l.N * l.H >= 256 || l.dv <= 64 ? WIDE : SPLIT, vec, s);
 }
 
 hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
@@ -1125,10 +1213,10 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     SweepArgs a = base;
     a.y = l.k; a.z = l.v; a.dx = dk; a.dz = dv;
     a.s_out = f.s_tab; a.tot = f.s_tot;
-    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
     a.y = l.q; a.z = l.d_o; a.rev = 1; a.u_scale = l.scale;
     a.s_out = f.d_tab; a.tot = f.d_tot;
-    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
     ScanArgs sc = {f.s_tab, f.s_tot, l.s0, f.s_fin, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
                    l.dk * l.dv, base.H, base.nseg, 0, l.la_tok, 0};
     if ((e = launch_scan(sc, s)) != hipSuccess) return e;
@@ -1141,19 +1229,19 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     a.out = l.dq; a.w = l.q; a.u = f.uq;
     a.s_in = f.s_tab; a.s_t = 1;
     a.p_scale = a.s_scale = l.scale;
-    if ((e = launch_typed<OUTM, 2, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<OUTM, 2, 3, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
     // dk
     a.x = l.v; a.y = l.d_o; a.z = l.q;
     a.out = l.dk_out; a.w = l.k; a.u = f.uk;
     a.s_in = f.d_tab; a.rev = 1;
     a.p_scale = a.u_scale = l.scale;
     a.s_scale = 1.f;
-    if ((e = launch_typed<OUTU, 2, 3, 3>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<OUTU, 2, 3, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
     // dv
     a.x = l.k; a.y = l.q; a.z = l.d_o; a.dx = dk; a.dz = dv;
     a.out = l.dv_out; a.w = nullptr; a.u = nullptr;
     a.s_t = 0;
-    if ((e = launch_typed<OUT, 2, 1, 2>(l, a, vec, s)) != hipSuccess) return e;
+    if ((e = launch_typed<OUT, 2, 1, 2>(l, a, TALL, vec, s)) != hipSuccess) return e;
 
     DecayArgs d = {f.uq, f.uk, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,
                    l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,
