@@ -26,7 +26,7 @@ template <>
 __device__ __forceinline__ float to_f32<uint16_t>(uint16_t x) { return bf16_to_f32(x); }
 
 template <class T, int VE>
-struct alignas(VE * sizeof(T)) Pack {
+struct alignas(VE * sizeof(T) < 16 ? VE * sizeof(T) : 16) Pack {
     T e[VE];
 };
 
@@ -49,11 +49,14 @@ __device__ __forceinline__ void store_pack(T *p, int c, int D, const float (&v)[
     }
     *reinterpret_cast<Pack<T, VE> *>(p + c) = t;
 }
-// the weight's elements (bf16 or fp32), `none` without one
+// the weight's elements at columns c .. (bf16 or fp32), `none` without one
 template <int VE>
 __device__ __forceinline__ void load_weight(const void *w, int w_bf16, int64_t row, int c, int D, float none, float (&v)[VE]) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) v[e] = w && c + e < D ? load_qkv(w, row * D + c + e, w_bf16) : none;
+    for (int e = 0; e < VE; ++e) v[e] = none;
+    if (!w || c >= D) return;
+    if (w_bf16) load_pack<uint16_t, VE>(static_cast<const uint16_t *>(w) + row * D, c, D, v);
+    else load_pack<float, VE>(static_cast<const float *>(w) + row * D, c, D, v);
 }
 
 // Sum over the lanes of a row: tpr neighbouring lanes of a wave, or (BLOCK,
@@ -71,61 +74,103 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float *red) {
     return v;
 }
 
+// Raw elements of a row as this lane holds them, so that the next row's loads
+// are in flight while a row is summed.
+template <class T, int VE, int NV>
+struct Row {
+    Pack<T, VE> p[NV];
+    __device__ __forceinline__ void load(const T *x, int l, int tpr, int D) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + l) * VE;
+            if (c < D) p[i] = *reinterpret_cast<const Pack<T, VE> *>(x + c);
+            else p[i] = Pack<T, VE>{};
+        }
+    }
+    __device__ __forceinline__ float at(int i, int e) const { return to_f32<T>(p[i].e[e]); }
+};
+
+// Each lane keeps the same columns of the same weight row for all its rows
+// (the launch steps by a multiple of G rows), so the weight is read once.
 template <class T, int VE, int NV, int BLOCK>
 __global__ void __launch_bounds__(BLOCK ? BLOCK : 256) norm_fwd_kernel(NormArgs a, int tpr) {
     __shared__ float red[16];
     const int D = static_cast<int>(a.D), l = BLOCK ? threadIdx.x : threadIdx.x % tpr;
     const int rows = BLOCK ? 1 : blockDim.x / tpr;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + (BLOCK ? 0 : threadIdx.x / tpr);
-    const bool live = row < a.rows;
-    const T *x = static_cast<const T *>(a.x) + (live ? row : 0) * D;
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * rows + (BLOCK ? 0 : threadIdx.x / tpr);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows, wr = a.G > 1 ? slot % a.G : 0;
     const float inv = 1.f / D;
-    float v[NV][VE], s = 0.f;
+    const T *x = static_cast<const T *>(a.x);
+    Row<T, VE, NV> cur, next;
+    // lanes past the last row read row 0 and store nothing
+    cur.load(x + (slot < a.rows ? slot : 0) * D, l, tpr, D);
+    float w[NV][VE], b[NV][VE];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        load_pack<T, VE>(x, live ? (i * tpr + l) * VE : D, D, v[i]);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) s += v[i][e];
+        load_weight<VE>(a.w, a.w_bf16, wr, (i * tpr + l) * VE, D, 1.f, w[i]);
+        load_weight<VE>(a.b, a.w_bf16, wr, (i * tpr + l) * VE, D, 0.f, b[i]);
     }
-    const float mean = row_sum<BLOCK>(s, tpr, red) * inv;
-    s = 0.f;
+    // every wave of a workgroup runs the same number of rounds
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * rows, row = slot; at < a.rows; at += step, row += step) {
+        if (at + step < a.rows) next.load(x + (row + step < a.rows ? row + step : 0) * D, l, tpr, D);
+        float v[NV][VE], s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            v[i][e] -= mean;
-            s += (i * tpr + l) * VE + e < D ? v[i][e] * v[i][e] : 0.f;
+            for (int e = 0; e < VE; ++e) {
+                v[i][e] = cur.at(i, e);
+                s += v[i][e];
+            }
+        const float mean = row_sum<BLOCK>(s, tpr, red) * inv;
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                v[i][e] -= mean;
+                s += (i * tpr + l) * VE + e < D ? v[i][e] * v[i][e] : 0.f;
+            }
+        const float rstd = 1.f / sqrtf(row_sum<BLOCK>(s, tpr, red) * inv + a.eps);
+        if (row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) v[i][e] = v[i][e] * rstd * w[i][e] + b[i][e];
+                store_pack<T, VE>(static_cast<T *>(a.y) + row * D, (i * tpr + l) * VE, D, v[i]);
+            }
+            if (l == 0) {
+                if (a.mean) a.mean[row] = mean;
+                if (a.rstd) a.rstd[row] = rstd;
+            }
         }
-    const float rstd = 1.f / sqrtf(row_sum<BLOCK>(s, tpr, red) * inv + a.eps);
-    if (!live) return;
-    const int64_t wr = a.G > 1 ? row % a.G : 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + l) * VE;
-        float w[VE], b[VE];
-        load_weight<VE>(a.w, a.w_bf16, wr, c, D, 1.f, w);
-        load_weight<VE>(a.b, a.w_bf16, wr, c, D, 0.f, b);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v[i][e] = v[i][e] * rstd * w[e] + b[e];
-        store_pack<T, VE>(static_cast<T *>(a.y) + row * D, c, D, v[i]);
-    }
-    if (l == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
+        cur = next;
     }
 }
 
-// Each lane keeps the same columns of the same weight row for all its rows
-// (the launch steps by a multiple of G rows), so its shares of dw and db stay
-// in registers; part[2][slots][D] takes them, slot = row slot of the launch.
+// As the forward; a lane's shares of dw and db stay in registers over all its
+// rows.  With one weight row for all, a workgroup adds its lanes' shares up
+// and stores one row of part[2][gridDim][D]; else every row slot stores its
+// own, part[2][gridDim * rows][D].
 template <class T, int VE, int NV, int BLOCK>
 __global__ void __launch_bounds__(BLOCK ? BLOCK : 256) norm_bwd_kernel(NormArgs a, int tpr, float *part) {
+    constexpr bool AHEAD = BLOCK != 1024;  // half the registers a lane: no room for a second row
     __shared__ float red[16];
+    extern __shared__ float share[];  // [4][D] (rows within waves, one weight row)
     const int D = static_cast<int>(a.D), l = BLOCK ? threadIdx.x : threadIdx.x % tpr;
     const int rows = BLOCK ? 1 : blockDim.x / tpr;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * rows + (BLOCK ? 0 : threadIdx.x / tpr);
-    const int64_t slots = static_cast<int64_t>(gridDim.x) * rows, wr = a.G > 1 ? slot % a.G : 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows, wr = a.G > 1 ? slot % a.G : 0;
     const float inv = 1.f / D;
+    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+    Row<T, VE, NV> cx, cy, nx, ny;
+    float mean, rstd, next_mean = 0.f, next_rstd = 0.f;
+    {
+        const int64_t r = slot < a.rows ? slot : 0;
+        cx.load(x + r * D, l, tpr, D);
+        cy.load(dy + r * D, l, tpr, D);
+        mean = a.mean[r];
+        rstd = a.rstd[r];
+    }
     float w[NV][VE], dw[NV][VE], db[NV][VE];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -133,29 +178,27 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : 256) norm_bwd_kernel(NormArgs 
 #pragma unroll
         for (int e = 0; e < VE; ++e) dw[i][e] = db[i][e] = 0.f;
     }
-    // every wave of a workgroup runs the same number of rounds
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * rows; at < a.rows; at += slots) {
-        const int64_t row = at + (BLOCK ? 0 : threadIdx.x / tpr);
-        const bool live = row < a.rows;
-        const int64_t r = live ? row : 0;
-        const float mean = a.mean[r], rstd = a.rstd[r];
-        float x[NV][VE], dy[NV][VE], s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * tpr + l) * VE;
-            load_pack<T, VE>(static_cast<const T *>(a.x) + r * D, live ? c : D, D, x[i]);
-            load_pack<T, VE>(static_cast<const T *>(a.dy) + r * D, live ? c : D, D, dy[i]);
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * rows, row = slot; at < a.rows; at += step, row += step) {
+        if (AHEAD && at + step < a.rows) {
+            const int64_t r = row + step < a.rows ? row + step : 0;
+            nx.load(x + r * D, l, tpr, D);
+            ny.load(dy + r * D, l, tpr, D);
+            next_mean = a.mean[r];
+            next_rstd = a.rstd[r];
         }
+        const bool live = row < a.rows;
+        float h[NV][VE], g[NV][VE], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                x[i][e] = (x[i][e] - mean) * rstd;  // xh; dy is zero outside the row
-                dw[i][e] += dy[i][e] * x[i][e];
-                db[i][e] += dy[i][e];
-                dy[i][e] *= w[i][e];
-                s1 += dy[i][e];
-                s2 += dy[i][e] * x[i][e];
+                const float d = live ? cy.at(i, e) : 0.f;  // zero outside the row too
+                h[i][e] = live ? (cx.at(i, e) - mean) * rstd : 0.f;
+                dw[i][e] += d * h[i][e];
+                db[i][e] += d;
+                g[i][e] = d * w[i][e];
+                s1 += g[i][e];
+                s2 += g[i][e] * h[i][e];
             }
         s1 = row_sum<BLOCK>(s1, tpr, red) * inv;
         s2 = row_sum<BLOCK>(s2, tpr, red) * inv;
@@ -163,34 +206,79 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : 256) norm_bwd_kernel(NormArgs 
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e) x[i][e] = rstd * (dy[i][e] - s1 - x[i][e] * s2);
-                store_pack<T, VE>(static_cast<T *>(a.dx) + row * D, (i * tpr + l) * VE, D, x[i]);
+                for (int e = 0; e < VE; ++e) h[i][e] = rstd * (g[i][e] - s1 - h[i][e] * s2);
+                store_pack<T, VE>(static_cast<T *>(a.dx) + row * D, (i * tpr + l) * VE, D, h[i]);
             }
         }
+        if (AHEAD) {
+            cx = nx;
+            cy = ny;
+            mean = next_mean;
+            rstd = next_rstd;
+        } else if (row + step < a.rows) {
+            cx.load(x + (row + step) * D, l, tpr, D);
+            cy.load(dy + (row + step) * D, l, tpr, D);
+            mean = a.mean[row + step];
+            rstd = a.rstd[row + step];
+        }
+    }
+    if (!BLOCK && a.G == 1) {
+        const int wave = threadIdx.x >> 6;
+        for (int which = 0; which < 2; ++which) {
+            if (!(which ? a.db : a.dw)) continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float v[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    v[e] = which ? db[i][e] : dw[i][e];
+                    for (int o = tpr; o < 64; o <<= 1) v[e] += __shfl_xor(v[e], o);
+                    const int c = (i * tpr + l) * VE + e;
+                    if ((threadIdx.x & 63) < static_cast<unsigned>(tpr) && c < D) share[wave * D + c] = v[e];
+                }
+            }
+            __syncthreads();
+            float *p = part + (which * static_cast<int64_t>(gridDim.x) + blockIdx.x) * D;
+            for (int c = threadIdx.x; c < D; c += 256) p[c] = (share[c] + share[D + c]) + (share[2 * D + c] + share[3 * D + c]);
+            __syncthreads();
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + l) * VE;
         if (a.dw) store_pack<float, VE>(part + slot * D, c, D, dw[i]);
-        if (a.db) store_pack<float, VE>(part + (slots + slot) * D, c, D, db[i]);
+        if (a.db) store_pack<float, VE>(part + (step + slot) * D, c, D, db[i]);
     }
 }
 
-// dw[g] = sum of the slots that hold weight row g, in a fixed order.
+// dw[g] = sum of the slots that hold weight row g, in a fixed order.  A
+// workgroup takes 16 columns, 64 lanes each a share of the slots.
 __global__ void __launch_bounds__(1024) norm_weight_kernel(NormArgs a, const float *part, int64_t slots, int blocks) {
-    __shared__ double red[16][64];
-    const int col = threadIdx.x & 63, r = threadIdx.x >> 6;
+    __shared__ double red[16][16];
+    const int col = threadIdx.x & 15, r = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int64_t g = blockIdx.x / blocks;
-    const int64_t c = static_cast<int64_t>(blockIdx.x % blocks) * 64 + col;
+    const int64_t c = static_cast<int64_t>(blockIdx.x % blocks) * 16 + col;
     const bool second = blockIdx.y == 1 || !a.dw;  // db
-    const float *p = part + (second ? slots * a.D : 0);
+    const float *p = part + (second ? slots * a.D : 0) + c;
     double s = 0.0;
-    if (c < a.D)
-        for (int64_t i = g + r * a.G; i < slots; i += 16 * a.G) s += p[i * a.D + c];
-    red[r][col] = s;
+    if (c < a.D) {
+        int64_t i = g + r * a.G;
+        for (; i + 192 * a.G < slots; i += 256 * a.G) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = p[(i + 64 * k * a.G) * a.D];
+            s += static_cast<double>(v[0]) + v[1] + v[2] + v[3];
+        }
+        for (; i < slots; i += 64 * a.G) s += p[i * a.D];
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if ((threadIdx.x & 63) < 16) red[wave][col] = s;
     __syncthreads();
-    if (r == 0 && c < a.D) {
-        for (int i = 1; i < 16; ++i) s += red[i][col];
+    if (threadIdx.x < 16 && c < a.D) {
+        s = 0.0;
+        for (int i = 0; i < 16; ++i) s += red[i][col];
         store_out(static_cast<float *>(second ? a.db : a.dw), g * a.D + c, static_cast<float>(s), a.w_bf16);
     }
 }
@@ -231,9 +319,9 @@ Plan plan_of(const NormArgs &a, bool vec) {
     return p;
 }
 
-// Workgroups of the backward: enough to fill the chip, and such that a step
-// of the launch is a multiple of G rows.
-int64_t bwd_grid(const NormArgs &a, const Plan &p) {
+// Workgroups of a launch: up to `want`, and such that a step of the launch is
+// a multiple of G rows.
+int64_t grid_of(const NormArgs &a, const Plan &p, int64_t want) {
     int64_t g = a.G, r = p.rows;
     while (r) {
         const int64_t t = g % r;
@@ -241,9 +329,16 @@ int64_t bwd_grid(const NormArgs &a, const Plan &p) {
         r = t;
     }
     const int64_t unit = a.G / g;  // G / gcd(G, rows)
-    const int64_t need = (a.rows + p.rows - 1) / p.rows, want = p.threads == 1024 ? 256 : 1024;
+    const int64_t need = (a.rows + p.rows - 1) / p.rows;
     const int64_t n = need < want ? need : want;
     return (n + unit - 1) / unit * unit;
+}
+int64_t fwd_grid(const NormArgs &a, const Plan &p) { return grid_of(a, p, p.threads == 1024 ? 512 : 2048); }
+int64_t bwd_grid(const NormArgs &a, const Plan &p) { return grid_of(a, p, p.threads == 1024 ? 256 : 1024); }
+
+// rows of the partial sums
+int64_t slots_of(const NormArgs &a, const Plan &p) {
+    return bwd_grid(a, p) * (a.G == 1 ? 1 : p.rows);
 }
 
 bool vector_ok(const NormArgs &a, std::initializer_list<const void *> ps) {
@@ -280,8 +375,8 @@ hipError_t dispatch(const Plan &p, F go) {
 
 template <class T>
 hipError_t fwd(const NormArgs &a, hipStream_t s) {
-    const Plan p = plan_of(a, vector_ok(a, {a.x, a.y}));
-    const int64_t grid = (a.rows + p.rows - 1) / p.rows;
+    const Plan p = plan_of(a, vector_ok(a, {a.x, a.y, a.w, a.b}));
+    const int64_t grid = fwd_grid(a, p);
     if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
     return dispatch<T>(p, [&](auto ve, auto nv, auto block) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, decltype(ve)::value, decltype(nv)::value, decltype(block)::value>),
@@ -292,15 +387,16 @@ hipError_t fwd(const NormArgs &a, hipStream_t s) {
 
 template <class T>
 hipError_t bwd(const NormArgs &a, float *part, hipStream_t s) {
-    const Plan p = plan_of(a, vector_ok(a, {a.x, a.dy, a.dx}));
-    const int64_t grid = bwd_grid(a, p), slots = grid * p.rows;
+    const Plan p = plan_of(a, vector_ok(a, {a.x, a.dy, a.dx, a.w}));
+    const int64_t grid = bwd_grid(a, p), slots = slots_of(a, p);
+    const size_t lds = !p.block && a.G == 1 ? 4 * a.D * sizeof(float) : 0;
     hipError_t e = dispatch<T>(p, [&](auto ve, auto nv, auto block) {
         hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(ve)::value, decltype(nv)::value, decltype(block)::value>),
-                           dim3(static_cast<unsigned>(grid)), dim3(p.threads), 0, s, a, p.tpr, part);
+                           dim3(static_cast<unsigned>(grid)), dim3(p.threads), lds, s, a, p.tpr, part);
         return hipGetLastError();
     });
     if (e != hipSuccess || (!a.dw && !a.db)) return e;
-    const int blocks = static_cast<int>((a.D + 63) / 64);
+    const int blocks = static_cast<int>((a.D + 15) / 16);
     if (a.G * blocks > 0x7fffffffLL) return hipErrorInvalidValue;
     hipLaunchKernelGGL(norm_weight_kernel, dim3(static_cast<unsigned>(a.G * blocks), a.dw && a.db ? 2 : 1), dim3(1024), 0, s,
                        a, part, slots, blocks);
@@ -314,7 +410,7 @@ size_t norm_bwd_workspace(const NormArgs &a) {
     size_t most = 0;
     for (bool vec : {false, true}) {
         const Plan p = plan_of(a, vec);
-        const size_t n = static_cast<size_t>(bwd_grid(a, p) * p.rows * a.D) * 8;
+        const size_t n = static_cast<size_t>(slots_of(a, p) * a.D) * 8;
         most = n > most ? n : most;
     }
     return most;

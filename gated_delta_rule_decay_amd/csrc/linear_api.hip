@@ -181,7 +181,7 @@ gdn2_status check_norm(const gdn2_norm_desc *d) {
     if (!(d->eps >= 0.f)) return GDN2_ERR_SHAPE;
     if (!product_ok({d->rows, d->dim, 16})) return GDN2_ERR_SHAPE;
     if (d->dim > 16384 || d->rows > INT32_MAX || !product_ok({d->groups, d->dim, 8}) ||
-        d->groups > INT32_MAX / ((d->dim + 63) / 64))
+        d->groups > INT32_MAX / ((d->dim + 15) / 16))
         return GDN2_ERR_UNSUPPORTED;
     return GDN2_OK;
 }
