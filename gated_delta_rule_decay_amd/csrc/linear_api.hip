@@ -69,12 +69,10 @@ gdn2_status check_linear(const gdn2_linear_desc *d, bool packed) {
     if (!product_ok({packed ? 1 : d->batch, d->seqlen, d->heads, dmax, 16}) ||
         !product_ok({d->batch, d->heads, d->dk, d->dv, 16}))
         return GDN2_ERR_SHAPE;
-    // launch sizes: 64 workgroups a state, two a segment of 256 tokens
-    const int64_t chains = d->batch * d->heads, rows = (packed ? 1 : d->batch) * d->heads;
+    // launch sizes: 64 workgroups a state, three a segment of 64 tokens
+    const int64_t chains = d->batch * d->heads, rows = (packed ? 1 : d->batch) * d->heads, segs = d->seqlen / 64 + 1;
     if (d->seqlen > INT32_MAX || chains > (INT32_MAX >> 6) || d->heads > 65535 ||  // 32-bit offsets inside a chunk
-       
-        rows > (INT64_C(1) << 62) / (d->seqlen / 256 + 1) ||
-        2 * (rows * (d->seqlen / 256 + 1) + chains + 8) > INT32_MAX)
+        rows > (INT64_C(1) << 40) / segs || 3 * (rows * segs + chains + 8) > INT32_MAX)
         return GDN2_ERR_UNSUPPORTED;
     return GDN2_OK;
 }

@@ -65,6 +65,7 @@ struct SweepArgs {
     int ncb;                 // column blocks
     int la_tok, rev;
     int s_t;                 // state stored [dz][dx] (the sweep's state is the transpose)
+    int gx, gz;              // bytes of one access to x and y rows, to z, w and out rows: 16, 4 or 2
     float p_scale, u_scale, s_scale;
 };
 
@@ -255,10 +256,10 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, int off, int a
     return __builtin_amdgcn_raw_buffer_load_b128(b, off, add, 0);
 }
 __device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t b, int off, int add) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, off, add, 0));
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, off, add, 0));
 }
 __device__ __forceinline__ void store4(float v, __amdgpu_buffer_rsrc_t b, int off, int add) {
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b, off, add, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), b, off, add, 0);
 }
 
 __device__ __forceinline__ bool inside(int p, int len) { return static_cast<unsigned>(p) < static_cast<unsigned>(len); }
@@ -276,48 +277,45 @@ struct Stage {
     int64_t row;    // elements from one position to the next
     int off;        // this thread's bytes in pass 0 (rev: in the last)
     int add0, step; // bytes of pass 0, from pass to pass
-    int r0, c, d;
+    int r0, c, d, gran;
 
-    __device__ __forceinline__ void init(const void *p, int64_t first, int H, int h, int d_, int col0, bool rev, int tid) {
+    __device__ __forceinline__ void init(const void *p, int64_t first, int H, int h, int d_, int col0, bool rev, int gran_, int tid) {
         d = d_;
+        gran = gran_;
         const int pitch = H * d;
         row = rev ? -static_cast<int64_t>(pitch) : pitch;
         base = static_cast<const T *>(p) + (first * H + h) * d;
         r0 = tid / Tl::UNITS;
         c = col0 + (tid % Tl::UNITS) * Tl::PER;
-        if (VEC) {
-            if (rev) base -= static_cast<int64_t>(CT - 1) * pitch;
-            off = c < d ? ((rev ? RX - 1 - r0 : r0) * pitch + c) * static_cast<int>(sizeof(T)) : NOWHERE;
-            step = (rev ? -RX : RX) * pitch * static_cast<int>(sizeof(T));
-            add0 = rev ? -(N - 1) * step : 0;
-        }
+        if (rev) base -= static_cast<int64_t>(CT - 1) * pitch;
+        off = c < d ? ((rev ? RX - 1 - r0 : r0) * pitch + c) * static_cast<int>(sizeof(T)) : NOWHERE;
+        step = (rev ? -RX : RX) * pitch * static_cast<int>(sizeof(T));
+        add0 = rev ? -(N - 1) * step : 0;
     }
     // positions p0 .. p0+CT-1, of which [0, len) exist
     __device__ __forceinline__ void load(int p0, int len) {
-        if (VEC) {
-            const auto b = buffer(base + p0 * row);
+        const auto b = buffer(base + p0 * row);
+        if (VEC || gran == 16) {
 #pragma unroll
             for (int i = 0; i < N; ++i) r[i] = load16(b, inside(p0 + r0 + i * RX, len) ? off : NOWHERE, add0 + i * step);
+        } else if (gran == 4) {
+            constexpr int PER4 = 4 / sizeof(T);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    r[i][k] = __builtin_amdgcn_raw_buffer_load_b32(
+                        b, inside(p0 + r0 + i * RX, len) && c + k * PER4 < d ? off + 4 * k : NOWHERE, add0 + i * step, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int p = p0 + r0 + i * RX;
-                u32x4 v = {0, 0, 0, 0};
-                if (inside(p, len) && c < d) {
-                    const T *s = base + p * row + c;
-                    if (sizeof(T) == 2) {
-                        const uint16_t *e = reinterpret_cast<const uint16_t *>(s);
+                uint32_t e[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (c + k < d) v[k >> 1] |= static_cast<uint32_t>(e[k]) << (16 * (k & 1));
-                    } else {
-                        const uint32_t *e = reinterpret_cast<const uint32_t *>(s);
+                for (int k = 0; k < 8; ++k)
+                    e[k] = __builtin_amdgcn_raw_buffer_load_b16(
+                        b, inside(p0 + r0 + i * RX, len) && c + k < d ? off + 2 * k : NOWHERE, add0 + i * step, 0);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (c + k < d) v[k] = e[k];
-                    }
-                }
-                r[i] = v;
+                for (int k = 0; k < 4; ++k) r[i][k] = (e[2 * k] & 0xffffu) | (e[2 * k + 1] << 16);
             }
         }
     }
@@ -484,10 +482,10 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 
     Stage<T, DX, CT, NTH, VEC> sx, sy;
     Stage<T, Sh::WC, CT, NTH, VEC> sz, sw;
-    sy.init(a.y, first, a.H, h, a.dx, 0, rev, tid);
-    sz.init(a.z, first, a.H, h, a.dz, col0, rev, tid);
-    if (MODE != STATE) sx.init(a.x, first, a.H, h, a.dx, 0, rev, tid);
-    if (MODE >= OUTU) sw.init(a.w, first, a.H, h, a.dz, col0, rev, tid);
+    sy.init(a.y, first, a.H, h, a.dx, 0, rev, a.gx, tid);
+    sz.init(a.z, first, a.H, h, a.dz, col0, rev, a.gz, tid);
+    if (MODE != STATE) sx.init(a.x, first, a.H, h, a.dx, 0, rev, a.gx, tid);
+    if (MODE >= OUTU) sw.init(a.w, first, a.H, h, a.dz, col0, rev, a.gz, tid);
     double total = 0.0;  // log2 decays of the staged chunks (last wave)
     float la_next = 0.f;
     // position p takes the decay of token first + p, or (rev) first - p + 1,
@@ -767,43 +765,46 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                     }
             {
                 T *o = obase + (rev ? -(p0 + CT - 1) : p0) * orow;
-                if constexpr (VEC) {
-                    const auto b = buffer(o);
+                const auto b = buffer(o);
 #pragma unroll
-                    for (int q = 0; q < RTW; ++q) {
-                        const int p = p0 + 16 * (rt0 + q) + ls;
-                        // 16-byte stores with a register as their uniform offset
-                        // have written registers that the next instruction
-                        // overwrote: the whole offset goes into the lane's
-                        const int off = inside(p, len) && ooff != NOWHERE
-                                            ? ooff + 16 * (rev ? RT - 1 - rt0 - q : rt0 + q) * static_cast<int>(orow) * ESZ
-                                            : NOWHERE;
-                        if constexpr (ESZ == 2) {
-                            uint32_t w[2 * NT];
+                for (int q = 0; q < RTW; ++q) {
+                    const int p = p0 + 16 * (rt0 + q) + ls;
+                    // 16-byte stores with a register as their uniform offset
+                    // have written registers that the next instruction
+                    // overwrote: the whole offset goes into the lane's
+                    const int off = inside(p, len) && ooff != NOWHERE
+                                        ? ooff + 16 * (rev ? RT - 1 - rt0 - q : rt0 + q) * static_cast<int>(orow) * ESZ
+                                        : NOWHERE;
+                    uint32_t w[NC * ESZ / 4];  // the row's outputs of this lane
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                w[2 * t] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{R[q][t][0], R[q][t][1]}), bf16x2));
-                                w[2 * t + 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{R[q][t][2], R[q][t][3]}), bf16x2));
-                            }
-                            if constexpr (NT == 2)
-                                __builtin_amdgcn_raw_buffer_store_b128((u32x4{w[0], w[1], w[2], w[3]}), b, off, 0, 0);
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; r += 4 / ESZ) {
+                            if constexpr (ESZ == 2)
+                                w[2 * t + r / 2] = __builtin_bit_cast(
+                                    uint32_t, __builtin_convertvector((f32x2{R[q][t][r], R[q][t][r + 1]}), bf16x2));
                             else
-                                __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[1]}), b, off, 0, 0);
-                        } else {
-#pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, R[q][t]), b,
-                                                                       t == 0 || oc + 4 < a.dz ? off + 16 * t : NOWHERE, 0, 0);
+                                w[4 * t + r] = __float_as_uint(R[q][t][r]);
                         }
-                    }
-                } else {
+                    if (VEC || a.gz == 16) {
+                        if constexpr (NC * ESZ == 8)
+                            __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[1]}), b, off, 0, 0);
+                        else
 #pragma unroll
-                    for (int q = 0; q < RTW; ++q) {
-                        const int i = 16 * (rt0 + q) + ls, p = p0 + i;
-                        if (inside(p, len))
+                            for (int k = 0; k < NC * ESZ / 4; k += 4)
+                                __builtin_amdgcn_raw_buffer_store_b128((u32x4{w[k], w[k + 1], w[k + 2], w[k + 3]}), b,
+                                                                       oc + 4 * k / ESZ < a.dz && off != NOWHERE ? off + 4 * k : NOWHERE, 0, 0);
+                    } else if (a.gz == 4) {
 #pragma unroll
-                            for (int n = 0; n < NC; ++n)
-                                if (oc + n < a.dz) o[(rev ? CT - 1 - i : i) * orow + oc + n] = static_cast<T>(R[q][n >> 2][n & 3]);
+                        for (int k = 0; k < NC * ESZ / 4; ++k)
+                            __builtin_amdgcn_raw_buffer_store_b32(
+                                w[k], b, oc + 4 * k / ESZ < a.dz && off != NOWHERE ? off + 4 * k : NOWHERE, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < NC; ++k)
+                            __builtin_amdgcn_raw_buffer_store_b16(
+                                static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1))), b,
+                                oc + k < a.dz && off != NOWHERE ? off + 2 * k : NOWHERE, 0, 0);
                     }
                 }
             }
@@ -847,6 +848,34 @@ __global__ void __launch_bounds__(64 * NCW * KSP, 2) sweep_kernel(SweepArgs a) {
     sweep_body<T, DX, NCW, NT, KSP, MODE, NP, NS, NU, VEC>(a, item, smem);
 }
 
+// The two state sweeps of the backward, and its three gradient sweeps, in one
+// launch each.  The sweeps of one segment and head read the same rows, so
+// they get neighbouring numbers on one XCD.
+struct Sweeps {
+    SweepArgs s[3];
+};
+
+template <class T, int DX, int NCW, bool VEC>
+__global__ void __launch_bounds__(64 * NCW, 2) state_pair_kernel(Sweeps a) {
+    extern __shared__ __align__(16) char smem[];
+    const int64_t q = blockIdx.x >> 3, sh = (q >> 1) * 8 + (blockIdx.x & 7);
+    if (sh >= a.s[0].segs * a.s[0].H) return;
+    sweep_body<T, DX, NCW, 1, 1, STATE, 1, 1, sizeof(T) == 2 ? 3 : 1, VEC>(a.s[q & 1], sh, smem);
+}
+
+template <class T, int DX, int NCW, bool VEC>
+__global__ void __launch_bounds__(64 * NCW, 2) gradient_kernel(Sweeps a) {
+    extern __shared__ __align__(16) char smem[];
+    constexpr bool B = sizeof(T) == 2;
+    const int64_t q = blockIdx.x >> 3, sh = (q / 3) * 8 + (blockIdx.x & 7);
+    if (sh >= a.s[0].segs * a.s[0].H) return;
+    switch (q % 3) {
+        case 0: sweep_body<T, DX, NCW, 1, 1, OUTM, B ? 2 : 1, B ? 3 : 1, B ? 3 : 1, VEC>(a.s[0], sh, smem); break;
+        case 1: sweep_body<T, DX, NCW, 1, 1, OUTU, B ? 2 : 1, B ? 3 : 1, B ? 3 : 1, VEC>(a.s[1], sh, smem); break;
+        default: sweep_body<T, DX, NCW, 1, 1, OUT, B ? 2 : 1, 1, B ? 2 : 1, VEC>(a.s[2], sh, smem); break;
+    }
+}
+
 // The scan over a sequence's segments: what each adds to the state becomes
 // the state that enters it, in place.  One lane per state element.
 struct ScanArgs {
@@ -862,7 +891,12 @@ struct ScanArgs {
     int H, nseg, rev, la_tok, blocks;  // blocks: workgroups of a state
 };
 
-__global__ void __launch_bounds__(256) segment_scan_kernel(ScanArgs a) {
+struct Scans {
+    ScanArgs s[2];
+};
+
+__global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
+    const ScanArgs &a = two.s[blockIdx.y];
     const int64_t sh = blockIdx.x / a.blocks, n = sh / a.H;
     const int h = static_cast<int>(sh - n * a.H);
     const int64_t e = static_cast<int64_t>(blockIdx.x % a.blocks) * 256 + threadIdx.x;
@@ -885,7 +919,7 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(ScanArgs a) {
 }
 
 // d la of a segment: its last token's <S, dS>, then back over the segment the
-// differences of the row products, in 64 bits.  One wave per (segment, head).
+// differences of the row products, in 64 bits.  One workgroup per (segment, head).
 struct DecayArgs {
     const float *uq, *uk;   // [H][tokens]
     const float *s_tab, *d_tab;  // states entering the segments, forward and reverse
@@ -934,33 +968,41 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs a) {
     for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
     if (lane == 0) red[tid >> 6] = x;
     __syncthreads();
-    if (tid >= 64) return;
     x = red[0] + red[1] + red[2] + red[3];
     // the reverse state has yet to pass the decay behind the segment
     if (!last) x *= exp(static_cast<double>(max(a.la[a.la_tok ? hi * a.H + h : h], LA_MIN)));
     double sum = 0.0;
-    for (int64_t top = hi; top > lo; top -= 64) {  // tokens top-1-lane
-        const int64_t t = top - 1 - lane;
-        double v = 0.0;
-        if (t >= lo) {
-            const int64_t at = static_cast<int64_t>(h) * a.tokens + t;
-            v = static_cast<double>(a.uq[at]) - static_cast<double>(a.uk[at]);
-        }
+    const float *uq = a.uq + static_cast<int64_t>(h) * a.tokens, *uk = a.uk + static_cast<int64_t>(h) * a.tokens;
+    for (int64_t top = hi; top > lo; top -= 1024) {  // tokens top-1-4 tid-j
+        double v[4];
+        const int64_t t0 = top - 1 - 4 * tid;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double up = __shfl_up(v, o);
-            if (lane >= o) v += up;
-        }
-        if (t >= lo) {
-            if (a.la_tok) a.d_la[t * a.H + h] = static_cast<float>(x + v);
-            sum += x + v;
-        }
-        x += __shfl(v, 63);
+        for (int j = 0; j < 4; ++j) v[j] = t0 - j >= lo ? static_cast<double>(uq[t0 - j]) - static_cast<double>(uk[t0 - j]) : 0.0;
+#pragma unroll
+        for (int j = 1; j < 4; ++j) v[j] += v[j - 1];
+        const double upto = wave_prefix(v[3]);
+        __syncthreads();  // the previous round's readers
+        if (lane == 63) red[tid >> 6] = upto;
+        __syncthreads();
+        double before = upto - v[3];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) before += w < (tid >> 6) ? red[w] : 0.0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (t0 - j >= lo) {
+                const double g = x + before + v[j];
+                if (a.la_tok) a.d_la[(t0 - j) * a.H + h] = static_cast<float>(g);
+                sum += g;
+            }
+        x += red[0] + red[1] + red[2] + red[3];
     }
     if (!a.la_tok) {
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-        if (lane == 0) a.part[sh] = sum;
+        __syncthreads();
+        if (lane == 0) red[tid >> 6] = sum;
+        __syncthreads();
+        if (tid == 0) a.part[sh] = red[0] + red[1] + red[2] + red[3];
     }
 }
 
@@ -979,8 +1021,6 @@ __global__ void __launch_bounds__(64) decay_sum_kernel(const double *part, const
 // ---- host side
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 struct Cut {
     int L;         // tokens of a segment
@@ -1001,7 +1041,7 @@ Cut fwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
     if (a.T <= 256 || heads >= 128) return Cut{0, 1, a.N};
     int64_t L = (a.T * heads / 512 + 63) / 64 * 64;
-    if (L < 256) L = 256;
+    if (L < 128) L = 128;
     if (!a.cu && L >= a.T) return Cut{0, 1, a.N};
     return cut_of(a, L);
 }
@@ -1010,8 +1050,8 @@ Cut fwd_cut(const LinArgs &a) {
 // which bounds how far the differences of the decay's gradient are summed.
 Cut bwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
-    int64_t L = (a.T * heads / 256 + 63) / 64 * 64;
-    if (L < 256) L = 256;
+    int64_t L = (a.T * heads / (a.dk > 64 || a.dv > 64 ? 256 : 768) + 63) / 64 * 64;
+    if (L < 64) L = 64;
     if (L > 1024) L = 1024;
     return cut_of(a, L);
 }
@@ -1089,20 +1129,64 @@ SweepArgs sweep_of(const LinArgs &l, const Cut &c, const VarPlan *vp) {
     return a;
 }
 
-bool vector_rows(const LinArgs &l, std::initializer_list<const void *> ps) {
-    const int per = l.bf16 ? 8 : 4;
-    bool ok = l.dk % per == 0 && l.dv % per == 0;
-    for (const void *p : ps) ok = ok && aligned16(p);
-    return ok;
+// Bytes of one access to rows of d elements at these addresses.
+int granularity(const LinArgs &l, int64_t d, std::initializer_list<const void *> ps) {
+    const int esz = l.bf16 ? 2 : 4;
+    int g = d * esz % 16 == 0 ? 16 : d * esz % 4 == 0 ? 4 : 2;
+    for (const void *p : ps) {
+        const uintptr_t u = reinterpret_cast<uintptr_t>(p);
+        if (g == 16 && u % 16 != 0) g = 4;
+        if (g == 4 && u % 4 != 0) g = 2;
+    }
+    return g;
 }
 
-hipError_t launch_scan(ScanArgs a, hipStream_t s) {
-    a.blocks = static_cast<int>((a.dkv + 255) / 256);
-    const int64_t grid = a.N * a.H * a.blocks;
+hipError_t launch_scans(Scans a, int n, hipStream_t s) {
+    for (int i = 0; i < n; ++i) a.s[i].blocks = static_cast<int>((a.s[i].dkv + 255) / 256);
+    const int64_t grid = a.s[0].N * a.s[0].H * a.s[0].blocks;
     if (grid <= 0) return hipSuccess;
     if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(segment_scan_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(segment_scan_kernel, dim3(static_cast<unsigned>(grid), n), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+template <class K>
+hipError_t launch_lds(K kernel, int64_t blocks, int threads, size_t lds, const Sweeps &a, hipStream_t s) {
+    if (blocks <= 0) return hipSuccess;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), lds, s, a);
+    return hipGetLastError();
+}
+
+// Both of the backward's launches for head sizes that share one shape: up to
+// 64 channels, or more, on both sides.
+template <class T, int D, bool VEC>
+hipError_t launch_states(const Sweeps &a, hipStream_t s) {
+    constexpr int NCW = D / 16;
+    using Sh = Shape<T, D, NCW, 1, 1>;
+    const int64_t groups = (a.s[0].segs * a.s[0].H + 7) / 8 * 8;
+    return launch_lds(state_pair_kernel<T, D, NCW, VEC>, 2 * groups, 64 * NCW, Sh::bytes(STATE, 1), a, s);
+}
+template <class T, int D, bool VEC>
+hipError_t launch_gradients(const Sweeps &a, hipStream_t s) {
+    constexpr int NCW = D / 16;
+    using Sh = Shape<T, D, NCW, 1, 1>;
+    const int64_t groups = (a.s[0].segs * a.s[0].H + 7) / 8 * 8;
+    return launch_lds(gradient_kernel<T, D, NCW, VEC>, 3 * groups, 64 * NCW, Sh::bytes(OUTM, sizeof(T) == 2 ? 2 : 1), a, s);
+}
+template <class T, int D>
+hipError_t launch_joint(bool states, const Sweeps &a, bool vec, hipStream_t s) {
+    if (states) return vec ? launch_states<T, D, true>(a, s) : launch_states<T, D, false>(a, s);
+    return vec ? launch_gradients<T, D, true>(a, s) : launch_gradients<T, D, false>(a, s);
+}
+hipError_t launch_joint(const LinArgs &l, bool states, const Sweeps &a, bool vec, hipStream_t s) {
+    if (l.dk > 64) return l.bf16 ? launch_joint<__bf16, 128>(states, a, vec, s) : launch_joint<float, 128>(states, a, vec, s);
+    return l.bf16 ? launch_joint<__bf16, 64>(states, a, vec, s) : launch_joint<float, 64>(states, a, vec, s);
 }
 
 struct Bump {
@@ -1180,16 +1264,18 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
     a.out = l.o;
     a.s_in = l.s0;
     a.s_out = l.s_out;
-    const bool vec = vector_rows(l, {l.q, l.k, l.v, l.o});
+    a.gx = granularity(l, l.dk, {l.q, l.k});
+    a.gz = granularity(l, l.dv, {l.v, l.o});
+    const bool vec = a.gx == 16 && a.gz == 16;
     if (cut) {
         SweepArgs st = a;
         st.s_in = nullptr;
         st.s_out = f.tab;
         st.tot = f.tot;
         if ((e = launch_typed<STATE, 1, 1, 3>(l, st, TALL, vec, s)) != hipSuccess) return e;
-        ScanArgs sc = {f.tab, f.tot, l.s0, l.s_out, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
+        const ScanArgs sc = {f.tab, f.tot, l.s0, l.s_out, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
                        l.dk * l.dv, a.H, a.nseg, 0, l.la_tok, 0};
-        if ((e = launch_scan(sc, s)) != hipSuccess) return e;
+        if ((e = launch_scans({{sc, {}}}, 1, s)) != hipSuccess) return e;
         a.s_in = f.tab;
         a.s_out = nullptr;
     }
@@ -1205,43 +1291,55 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     hipError_t e;
     VarPlan vp;
     if (l.cu && (e = launch_varlen_plan(l.cu, l.N, l.T, c.L, f.plan, &vp, s)) != hipSuccess) return e;
-    const SweepArgs base = sweep_of(l, c, l.cu ? &vp : nullptr);
-    const bool vec = vector_rows(l, {l.q, l.k, l.v, l.d_o, l.dq, l.dk_out, l.dv_out});
+    SweepArgs base = sweep_of(l, c, l.cu ? &vp : nullptr);
+    base.ncb = 1;
     const int dk = static_cast<int>(l.dk), dv = static_cast<int>(l.dv);
+    const int gk = granularity(l, dk, {l.q, l.k, l.dq, l.dk_out}), gv = granularity(l, dv, {l.v, l.d_o, l.dv_out});
+    const bool vec = gk == 16 && gv == 16, joint = (dk > 64) == (dv > 64);
 
     // what the segments add to the state, and in reverse to its gradient
-    SweepArgs a = base;
-    a.y = l.k; a.z = l.v; a.dx = dk; a.dz = dv;
-    a.s_out = f.s_tab; a.tot = f.s_tot;
-    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
-    a.y = l.q; a.z = l.d_o; a.rev = 1; a.u_scale = l.scale;
-    a.s_out = f.d_tab; a.tot = f.d_tot;
-    if ((e = launch_typed<STATE, 1, 1, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
-    ScanArgs sc = {f.s_tab, f.s_tot, l.s0, f.s_fin, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
-                   l.dk * l.dv, base.H, base.nseg, 0, l.la_tok, 0};
-    if ((e = launch_scan(sc, s)) != hipSuccess) return e;
-    sc.tab = f.d_tab; sc.tot = f.d_tot; sc.init = l.d_sT; sc.fin = l.d_s0; sc.rev = 1;
-    if ((e = launch_scan(sc, s)) != hipSuccess) return e;
+    Sweeps w = {{base, base, base}};
+    w.s[0].y = l.k; w.s[0].z = l.v; w.s[0].dx = dk; w.s[0].dz = dv; w.s[0].gx = gk; w.s[0].gz = gv;
+    w.s[0].s_out = f.s_tab; w.s[0].tot = f.s_tot;
+    w.s[1] = w.s[0];
+    w.s[1].y = l.q; w.s[1].z = l.d_o; w.s[1].rev = 1; w.s[1].u_scale = l.scale;
+    w.s[1].s_out = f.d_tab; w.s[1].tot = f.d_tot;
+    if (joint) {
+        if ((e = launch_joint(l, true, w, vec, s)) != hipSuccess) return e;
+    } else {
+        for (int i = 0; i < 2; ++i)
+            if ((e = launch_typed<STATE, 1, 1, 3>(l, w.s[i], TALL, vec, s)) != hipSuccess) return e;
+    }
+    Scans sc;
+    sc.s[0] = {f.s_tab, f.s_tot, l.s0, f.s_fin, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
+               l.dk * l.dv, base.H, base.nseg, 0, l.la_tok, 0};
+    sc.s[1] = sc.s[0];
+    sc.s[1].tab = f.d_tab; sc.s[1].tot = f.d_tot; sc.s[1].init = l.d_sT; sc.s[1].fin = l.d_s0; sc.s[1].rev = 1;
+    if ((e = launch_scans(sc, 2, s)) != hipSuccess) return e;
 
-    // dq
-    a = base;
-    a.x = l.d_o; a.y = l.v; a.z = l.k; a.dx = dv; a.dz = dk;
-    a.out = l.dq; a.w = l.q; a.u = f.uq;
-    a.s_in = f.s_tab; a.s_t = 1;
-    a.p_scale = a.s_scale = l.scale;
-    if ((e = launch_typed<OUTM, 2, 3, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
-    // dk
-    a.x = l.v; a.y = l.d_o; a.z = l.q;
-    a.out = l.dk_out; a.w = l.k; a.u = f.uk;
-    a.s_in = f.d_tab; a.rev = 1;
-    a.p_scale = a.u_scale = l.scale;
-    a.s_scale = 1.f;
-    if ((e = launch_typed<OUTU, 2, 3, 3>(l, a, TALL, vec, s)) != hipSuccess) return e;
-    // dv
-    a.x = l.k; a.y = l.q; a.z = l.d_o; a.dx = dk; a.dz = dv;
-    a.out = l.dv_out; a.w = nullptr; a.u = nullptr;
-    a.s_t = 0;
-    if ((e = launch_typed<OUT, 2, 1, 2>(l, a, TALL, vec, s)) != hipSuccess) return e;
+    w = {{base, base, base}};
+    SweepArgs &q = w.s[0], &k = w.s[1], &v = w.s[2];
+    q.x = l.d_o; q.y = l.v; q.z = l.k; q.dx = dv; q.dz = dk; q.gx = gv; q.gz = gk;
+    q.s_t = 1;
+    k = q;
+    q.out = l.dq; q.w = l.q; q.u = f.uq;
+    q.s_in = f.s_tab;
+    q.p_scale = q.s_scale = l.scale;
+    k.x = l.v; k.y = l.d_o; k.z = l.q;
+    k.out = l.dk_out; k.w = l.k; k.u = f.uk;
+    k.s_in = f.d_tab; k.rev = 1;
+    k.p_scale = k.u_scale = l.scale;
+    v.x = l.k; v.y = l.q; v.z = l.d_o; v.dx = dk; v.dz = dv; v.gx = gk; v.gz = gv;
+    v.out = l.dv_out;
+    v.s_in = f.d_tab; v.rev = 1;
+    v.p_scale = v.u_scale = l.scale;
+    if (joint) {
+        if ((e = launch_joint(l, false, w, vec, s)) != hipSuccess) return e;
+    } else {
+        if ((e = launch_typed<OUTM, 2, 3, 3>(l, q, TALL, vec, s)) != hipSuccess) return e;
+        if ((e = launch_typed<OUTU, 2, 3, 3>(l, k, TALL, vec, s)) != hipSuccess) return e;
+        if ((e = launch_typed<OUT, 2, 1, 2>(l, v, TALL, vec, s)) != hipSuccess) return e;
+    }
 
     DecayArgs d = {f.uq, f.uk, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,
                    l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,

@@ -8,8 +8,9 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 
-from .binding import GDN2_BF16, GDN2_F32, Gdn2Error, _check, _ptr, load_library
+from .binding import GDN2_BF16, GDN2_F32, Gdn2Error, _check, load_library
 
 GDN2_DECAY_TOKEN, GDN2_DECAY_HEAD = 0, 1
 
@@ -30,11 +31,15 @@ class Gdn2NormDesc(ctypes.Structure):
     ]
 
 
+_calls = {}  # entry point -> ctypes function
+
+
 def _lib():
     lib = load_library()
-    if not getattr(lib, "_linear_ready", False):
+    if not _calls:
         vp, sz = ctypes.c_void_p, ctypes.c_size_t
         ld, nd, szp = ctypes.POINTER(Gdn2LinearDesc), ctypes.POINTER(Gdn2NormDesc), ctypes.POINTER(ctypes.c_size_t)
+        ready = {}
         for name, args in (
                 ("gdn2_linear_fwd_workspace", [ld, szp]), ("gdn2_linear_fwd", [ld] + [vp] * 8 + [sz, vp]),
                 ("gdn2_linear_fwd_varlen_workspace", [ld, szp]),
@@ -47,31 +52,65 @@ def _lib():
                 ("gdn2_layer_norm_bwd", [nd] + [vp] * 9 + [sz, vp])):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = ctypes.c_int, args
-        lib._linear_ready = True
+            ready[name] = fn
+        _calls.update(ready)
     return lib
+
+
+def _call(name):
+    if not _calls:
+        _lib()
+    return _calls[name]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(index):
+    """torch's current stream of a device, as a hipStream_t."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _like(t, name, shape, dtype, dev):
+    """`_check` for one dtype, its four questions asked at once where all hold."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check(t, name, shape, (dtype,), dev)
 
 
 def _run(name, dev, desc, *args):
     """Call an entry point on `dev`'s current stream; raises on a bad status."""
     import torch
-    fn = getattr(_lib(), name)
+    fn = _call(name)
     if dev.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a GPU, not on {dev}")
     if torch.cuda.current_device() == dev.index:
-        st = fn(ctypes.byref(desc), *args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(desc, *args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(ctypes.byref(desc), *args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(desc, *args, _raw_stream(dev.index))
     if st != 0:
         raise Gdn2Error(st, name)
 
 
 def _bytes(name, desc):
     n = ctypes.c_size_t(0)
-    st = getattr(_lib(), name)(ctypes.byref(desc), ctypes.byref(n))
+    st = _call(name)(desc, ctypes.byref(n))
     if st != 0:
         raise Gdn2Error(st, name)
     return int(n.value)
+
+
+@functools.lru_cache(maxsize=256)
+def _need(name, make, *sizes):
+    """Workspace bytes of a request, which depend on its sizes alone."""
+    return _bytes(name, make(*sizes))
 
 
 def _dtype_code(t, name):
@@ -92,16 +131,17 @@ def make_norm_desc(rows, groups, dim, dtype=GDN2_BF16, weight_dtype=GDN2_F32, ep
     return Gdn2NormDesc(rows, groups, dim, dtype, weight_dtype, eps, 0)
 
 
-def _desc(q, k, v, log_decay, tok, batch, seqlen, q_scale):
+def _sizes(q, k, v, log_decay, tok, batch, seqlen, q_scale):
+    """What make_linear_desc takes, of checked inputs."""
     import torch
     H, dk, dv, dev = tok[-1], k.shape[-1], v.shape[-1], k.device
     code = _dtype_code(k, "q/k/v")
     for t, n, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv)):
-        _check(t, n, tok + (d,), (k.dtype,), dev)
+        _like(t, n, tok + (d,), k.dtype, dev)
     # [H]: one value per head; a per-token decay has all of tok's axes
     kind = GDN2_DECAY_HEAD if log_decay.dim() == 1 else GDN2_DECAY_TOKEN
-    _check(log_decay, "log_decay", (H,) if kind == GDN2_DECAY_HEAD else tok, (torch.float32,), dev)
-    return make_linear_desc(batch, seqlen, H, dk, dv, code, kind, q_scale)
+    _like(log_decay, "log_decay", (H,) if kind == GDN2_DECAY_HEAD else tok, torch.float32, dev)
+    return batch, seqlen, H, dk, dv, code, kind, q_scale
 
 
 def _packed(k, cu_seqlens):
@@ -152,22 +192,22 @@ def _fwd(q, k, v, log_decay, cu_seqlens, state0, q_scale, out, state_out, return
         tok, N, T = tuple(k.shape[:-1]), k.shape[0], k.shape[1]
     else:
         tok, N, T = _packed(k, cu_seqlens)
-    desc = _desc(q, k, v, log_decay, tok, N, T, q_scale)
-    dev, sshape, f32 = k.device, (N, tok[-1], k.shape[-1], v.shape[-1]), (torch.float32,)
+    sizes = _sizes(q, k, v, log_decay, tok, N, T, q_scale)
+    dev, sshape, f32 = k.device, (N, tok[-1], k.shape[-1], v.shape[-1]), torch.float32
     if state0 is not None:
-        _check(state0, "state0", sshape, f32, dev)
+        _like(state0, "state0", sshape, f32, dev)
     if out is None:
         out = torch.empty_like(v)
     else:
-        _check(out, "out", tuple(v.shape), (v.dtype,), dev)
+        _like(out, "out", v.shape, v.dtype, dev)
     if state_out is not None:
-        _check(state_out, "state_out", sshape, f32, dev)
+        _like(state_out, "state_out", sshape, f32, dev)
     elif return_state:
         state_out = torch.empty(sshape, dtype=torch.float32, device=dev)
     name = "gdn2_linear_fwd" if cu_seqlens is None else "gdn2_linear_fwd_varlen"
     ws, n = (None, 0) if workspace is False else _space(None if workspace is True else workspace,
-                                                        _bytes(name + "_workspace", desc), dev)
-    _run(name, dev, desc, *([] if cu_seqlens is None else [_ptr(cu_seqlens)]), _ptr(q), _ptr(k), _ptr(v),
+                                                        _need(name + "_workspace", make_linear_desc, *sizes[:-1]), dev)
+    _run(name, dev, make_linear_desc(*sizes), *([] if cu_seqlens is None else [_ptr(cu_seqlens)]), _ptr(q), _ptr(k), _ptr(v),
          _ptr(log_decay), _ptr(state0), _ptr(out), _ptr(state_out), _ptr(ws), n)
     return out, state_out
 
@@ -204,20 +244,20 @@ def _bwd(q, k, v, log_decay, cu_seqlens, state0, d_o, d_state, q_scale, want_sta
         tok, N, T = tuple(k.shape[:-1]), k.shape[0], k.shape[1]
     else:
         tok, N, T = _packed(k, cu_seqlens)
-    desc = _desc(q, k, v, log_decay, tok, N, T, q_scale)
-    dev, sshape, f32 = k.device, (N, tok[-1], k.shape[-1], v.shape[-1]), (torch.float32,)
-    _check(d_o, "d_o", tuple(v.shape), (v.dtype,), dev)
+    sizes = _sizes(q, k, v, log_decay, tok, N, T, q_scale)
+    dev, sshape, f32 = k.device, (N, tok[-1], k.shape[-1], v.shape[-1]), torch.float32
+    _like(d_o, "d_o", v.shape, v.dtype, dev)
     for t, n in ((state0, "state0"), (d_state, "d_state")):
         if t is not None:
-            _check(t, n, sshape, f32, dev)
+            _like(t, n, sshape, f32, dev)
     if want_state0 is None:
         want_state0 = state0 is not None
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
              d_log_decay=torch.empty_like(log_decay),
              d_state0=torch.empty(sshape, dtype=torch.float32, device=dev) if want_state0 else None)
     name = "gdn2_linear_bwd" if cu_seqlens is None else "gdn2_linear_bwd_varlen"
-    ws, n = _space(workspace, _bytes(name + "_workspace", desc), dev)
-    _run(name, dev, desc, *([] if cu_seqlens is None else [_ptr(cu_seqlens)]), _ptr(q), _ptr(k), _ptr(v),
+    ws, n = _space(workspace, _need(name + "_workspace", make_linear_desc, *sizes[:-1]), dev)
+    _run(name, dev, make_linear_desc(*sizes), *([] if cu_seqlens is None else [_ptr(cu_seqlens)]), _ptr(q), _ptr(k), _ptr(v),
          _ptr(log_decay), _ptr(state0), _ptr(d_o), _ptr(d_state), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
          _ptr(g["d_log_decay"]), _ptr(g["d_state0"]), _ptr(ws), n)
     return g
@@ -250,23 +290,23 @@ def linear_recurrent_step(q, k, v, log_decay, state, q_scale=1.0, out=None):
     if k.dim() != 3:
         raise ValueError("k is [N,H,dk]")
     tok = tuple(k.shape[:-1])
-    desc = _desc(q, k, v, log_decay, tok, tok[0], 1, q_scale)
-    _check(state, "state", tok + (k.shape[-1], v.shape[-1]), (torch.float32,), k.device)
+    sizes = _sizes(q, k, v, log_decay, tok, tok[0], 1, q_scale)
+    _like(state, "state", tok + (k.shape[-1], v.shape[-1]), torch.float32, k.device)
     if out is None:
         out = torch.empty_like(v)
     else:
-        _check(out, "out", tuple(v.shape), (v.dtype,), k.device)
-    _run("gdn2_linear_step", k.device, desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out))
+        _like(out, "out", v.shape, v.dtype, k.device)
+    _run("gdn2_linear_step", k.device, make_linear_desc(*sizes), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out))
     return out
 
 
-def _norm_desc(x, weight, bias, eps):
-    import torch
+def _norm_sizes(x, weight, bias, eps):
+    """What make_norm_desc takes, of checked inputs."""
     if x.dim() < 1:
         raise ValueError("x needs an axis to normalise")
     D = x.shape[-1]
     code = _dtype_code(x, "x")
-    _check(x, "x", tuple(x.shape), (x.dtype,), x.device)
+    _like(x, "x", x.shape, x.dtype, x.device)
     groups, wd = 1, GDN2_F32
     first = weight if weight is not None else bias
     if first is not None:
@@ -276,11 +316,11 @@ def _norm_desc(x, weight, bias, eps):
         shape = (D,) if first.dim() == 1 else (groups, D)
         for t, n in ((weight, "weight"), (bias, "bias")):
             if t is not None:
-                _check(t, n, shape, (first.dtype,), x.device)
+                _like(t, n, shape, first.dtype, x.device)
     rows = 1
     for n in x.shape[:-1]:
         rows *= n
-    return make_norm_desc(rows, max(groups, 1), D, code, wd, eps)
+    return rows, max(groups, 1), D, code, wd, eps
 
 
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
@@ -291,14 +331,14 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     fp32 of x's shape without its last axis.
     """
     import torch
-    desc = _norm_desc(x, weight, bias, eps)
+    sizes = _norm_sizes(x, weight, bias, eps)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _check(out, "out", tuple(x.shape), (x.dtype,), x.device)
-    stats = torch.empty((2,) + tuple(x.shape[:-1]), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    _run("gdn2_layer_norm_fwd", x.device, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd))
+        _like(out, "out", x.shape, x.dtype, x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _run("gdn2_layer_norm_fwd", x.device, make_norm_desc(*sizes), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd))
     return out, mean, rstd
 
 
@@ -312,11 +352,11 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, want_weight=None, want_bias=False,
     layer_norm_bwd_workspace() bytes.
     """
     import torch
-    desc = _norm_desc(x, weight, None, 0.0)
-    dev, stat = x.device, tuple(x.shape[:-1])
-    _check(dy, "dy", tuple(x.shape), (x.dtype,), dev)
-    _check(mean, "mean", stat, (torch.float32,), dev)
-    _check(rstd, "rstd", stat, (torch.float32,), dev)
+    sizes = _norm_sizes(x, weight, None, 0.0)
+    dev, stat = x.device, x.shape[:-1]
+    _like(dy, "dy", x.shape, x.dtype, dev)
+    _like(mean, "mean", stat, torch.float32, dev)
+    _like(rstd, "rstd", stat, torch.float32, dev)
     if want_weight is None:
         want_weight = weight is not None
 
@@ -327,7 +367,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, want_weight=None, want_bias=False,
     dw, db = like() if want_weight else None, like() if want_bias else None
     ws, n = None, 0
     if want_weight or want_bias or workspace is not None:
-        ws, n = _space(workspace, _bytes("gdn2_layer_norm_bwd_workspace", desc), dev)
-    _run("gdn2_layer_norm_bwd", dev, desc, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw),
+        ws, n = _space(workspace, _need("gdn2_layer_norm_bwd_workspace", make_norm_desc, *sizes[:-1]), dev)
+    _run("gdn2_layer_norm_bwd", dev, make_norm_desc(*sizes), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw),
          _ptr(db), _ptr(ws), n)
     return dx, dw, db
