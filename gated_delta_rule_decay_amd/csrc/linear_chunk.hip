@@ -355,6 +355,17 @@ __device__ __forceinline__ float row16_sum(float v) {
     return v;
 }
 
+// Sum over 4 or 8 neighbouring lanes, on each of them.
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+    static_assert(N == 4 || N == 8, "lanes of a half row");
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xb1, 0xf, 0xf, false));  // lane ^ 1
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4e, 0xf, 0xf, false));  // lane ^ 2
+    if (N == 8)  // the mirrored lane of eight, in the other four
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xf, 0xf, false));
+    return v;
+}
+
 // What a sweep does: its output parts.
 constexpr int STATE = 0;  // the state only
 constexpr int OUT = 1;    // outputs (and the state)
@@ -370,8 +381,8 @@ struct Shape {
     static constexpr int OB = KSP > 1 ? NW * (CT / 32) * NT * 1024 : 0;  // read sums passed between waves
     static constexpr size_t bytes(int mode, int np) {
         return CT * 8 + 2 * CT * 4 + 16 + (mode == STATE ? 1 : 2) * XB + (mode >= OUTU ? 2 : 1) * ZB +
-               (mode == STATE ? 0 : np * Scores<T>::BYTES + OB) + (mode >= OUTU ? NW * CT * 4 : 0) +
-               (mode == OUTM ? (CT / 16 + 1) * CT * 4 : 0);
+               (mode == STATE ? 0 : np * Scores<T>::BYTES + OB) + (mode >= OUTU ? NW * CT * 16 : 0) +
+               (mode == OUTM ? (CT / 16 + 1) * CT * 16 : 0);
     }
 };
 
@@ -428,10 +439,12 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     char *s_x = s_z + Sh::ZB;
     char *s_p = s_x + Sh::XB;
     char *s_w = s_p + NP * Sc::BYTES;
-    float *s_u = reinterpret_cast<float *>(s_w + Sh::ZB);  // [NW][CT]
-    float *s_m = s_u + (MODE >= OUTU ? NW * CT : 0);  // [CT/16 blocks][CT/16 + 1][16]: row sums of the block's tiles, then column sums
-
-    float *s_o = MODE >= OUTU ? s_m + (MODE == OUTM ? (RT + 1) * CT : 0) : reinterpret_cast<float *>(s_w);  // [NW][RTW][NT][64 lanes][4]
+    float *s_u = reinterpret_cast<float *>(s_w + Sh::ZB);  // [NW][CT][4 lane groups]
+    // [CT/16 blocks][CT/16 + 1][4][16]: sums of the block's tiles over their
+    // rows' four lane groups, then over their columns (one of the four)
+    float *s_m = s_u + (MODE >= OUTU ? 4 * NW * CT : 0);
+    // [NW][RTW][NT][64 lanes][4]
+    float *s_o = MODE >= OUTU ? s_m + (MODE == OUTM ? 4 * (RT + 1) * CT : 0) : reinterpret_cast<float *>(s_w);
 
     // column of slot s of tile t, relative to the wave's
     auto zcol = [](int t, int s) { return NT == 2 ? 8 * (s >> 2) + 4 * t + (s & 3) : s; };
@@ -494,10 +507,12 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     const float *la_base = a.la + h + (rev ? first + 1 - (CT - 1) : first) * la_pitch;
     const int la_off = static_cast<int>(rev ? CT - 1 - lane : lane) * static_cast<int>(la_pitch) * 4;
     const int la_skip = rev && sg.hi == sg.end ? -1 : 0;  // position 0 has none
-    auto load_chunk = [&](int p0) {
+    auto load_first = [&](int p0) {
         sy.load(p0, len);
-        sz.load(p0, len);
         if (MODE != STATE) sx.load(p0, len);
+    };
+    auto load_second = [&](int p0) {
+        sz.load(p0, len);
         if (MODE >= OUTU) sw.load(p0, len);
         if (wave == NW - 1)  // the decay of each position
             la_next = load4(buffer(la_base + p0 * la_row), inside(p0 + lane + la_skip, len + la_skip) && lane < CT ? la_off : NOWHERE, 0);
@@ -532,13 +547,17 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     // chunks keep the forward order's borders: in reverse the ragged one is first
     const int begin = rev ? -((CT - len % CT) % CT) : 0;
     if (len > 0) {
-        load_chunk(begin);
+        load_first(begin);
+        load_second(begin);
         stage_chunk();
     }
     __syncthreads();
 
     for (int p0 = begin; p0 < len; p0 += CT) {
-        if (p0 + CT < len) load_chunk(p0 + CT);
+        // the next chunk's loads, in two parts: a CU takes 64 bytes a cycle
+        const bool more = p0 + CT < len;
+        if (more) load_first(p0 + CT);
+        if (MODE == STATE && more) load_second(p0 + CT);
 
         Frag zf[KT][NT];
 #pragma unroll
@@ -567,7 +586,16 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                                 TX::row_frag(s_x + 16 * it * TX::BYTES, ls, 4 * ks + g), sc);
                 return sc;
             };
-            auto finish = [&](int it, int jt, f32x4 sc) {
+            auto pairs = [&](int it, int jt) {  // w_i . z_j
+                f32x4 m = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (MODE == OUTM)
+#pragma unroll
+                    for (int ks = 0; ks < Sh::WC / 32; ++ks)
+                        m = E::mma(TZ::row_frag(s_z + 16 * jt * TZ::BYTES, ls, 4 * ks + g),
+                                   TZ::row_frag(s_w + 16 * it * TZ::BYTES, ls, 4 * ks + g), m);
+                return m;
+            };
+            auto finish = [&](int it, int jt, f32x4 sc, f32x4 m) {
                 const int i = 16 * it + ls, j = 16 * jt + 4 * g;
                 const double gi = s_g[i];
                 f32x4 pr;
@@ -597,11 +625,6 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                     *reinterpret_cast<f32x4 *>(s_p + Sc::at(0, i, j >> 2)) = pr;
                 }
                 if constexpr (MODE == OUTM) {
-                    f32x4 m = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int ks = 0; ks < Sh::WC / 32; ++ks)
-                        m = E::mma(TZ::row_frag(s_z + 16 * jt * TZ::BYTES, ls, 4 * ks + g),
-                                   TZ::row_frag(s_w + 16 * it * TZ::BYTES, ls, 4 * ks + g), m);
                     float rs = 0.f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -609,28 +632,29 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                         rs += m[r];
                         m[r] = row16_sum(m[r]);
                     }
-                    rs += __shfl_xor(rs, 16);
-                    rs += __shfl_xor(rs, 32);
-                    if (g == 0) s_m[(it * (RT + 1) + jt) * 16 + ls] = rs;
-                    if (ls == 15) *reinterpret_cast<f32x4 *>(s_m + (jt * (RT + 1) + it + 1) * 16 + 4 * g) = m;
+                    s_m[((it * (RT + 1) + jt) * 4 + g) * 16 + ls] = rs;
+                    if (ls == 15) *reinterpret_cast<f32x4 *>(s_m + (jt * (RT + 1) + it + 1) * 64 + 4 * g) = m;
                 }
             };
             auto tile_i = [&](int n) { return static_cast<int>((0x3333222110ull >> (4 * n)) & 15); };
             auto tile_j = [&](int n) { return static_cast<int>((0x3210210100ull >> (4 * n)) & 15); };
-            if constexpr (KSP > 1) {  // one workgroup a CU: all at once, branch-free
-                f32x4 sc[MINE];
+            if constexpr (NW == 8) {  // one workgroup a CU: all at once, branch-free
+                f32x4 sc[MINE], m[MINE];
                 int n[MINE];
 #pragma unroll
                 for (int u = 0; u < MINE; ++u) {
                     n[u] = min(wave + u * NW, TILES - 1);
                     sc[u] = product(tile_i(n[u]), tile_j(n[u]));
+                    m[u] = pairs(tile_i(n[u]), tile_j(n[u]));
                 }
 #pragma unroll
-                for (int u = 0; u < MINE; ++u) finish(tile_i(n[u]), tile_j(n[u]), sc[u]);
+                for (int u = 0; u < MINE; ++u) finish(tile_i(n[u]), tile_j(n[u]), sc[u], m[u]);
             } else {  // two: one by one, in fewer registers
 #pragma unroll 1
-                for (int n = wave; n < TILES; n += NW) finish(tile_i(n), tile_j(n), product(tile_i(n), tile_j(n)));
+                for (int n = wave; n < TILES; n += NW) finish(tile_i(n), tile_j(n), product(tile_i(n), tile_j(n)), pairs(tile_i(n), tile_j(n)));
             }
+
+            if (more) load_second(p0 + CT);
 
             // outputs, transposed: x S first, which needs no scores
 #pragma unroll
@@ -669,9 +693,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 #pragma unroll
                         for (int r = 0; r < 4; ++r) us += O[rt][t][r] * w[r];
                     }
-                    us += __shfl_xor(us, 16);
-                    us += __shfl_xor(us, 32);
-                    if (g == 0) s_u[wave * CT + 16 * rt + ls] = us;
+                    s_u[(wave * CT + 16 * rt + ls) * 4 + g] = us;
                 }
             }
             if constexpr (KSP > 1)  // the other half's row tiles go to the wave that finishes them
@@ -716,25 +738,27 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
         }
 
         __syncthreads();  // the scores are written, the tiles read
-        if (p0 + CT < len) stage_chunk();
+        if (more) stage_chunk();
 
         if constexpr (MODE != STATE) {
-            if constexpr (MODE >= OUTU) {
-                const int p = p0 + tid;
-                if (tid < CT && inside(p, len)) {
-                    float us = 0.f;
-#pragma unroll
-                    for (int q = 0; q < NW; ++q) us += s_u[q * CT + tid];
+            if constexpr (MODE >= OUTU) {  // NW neighbouring lanes a token
+                const int i = tid / NW, part = tid % NW, p = p0 + i;
+                float us = 0.f;
+                if (i < CT) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(s_u + (part * CT + i) * 4);
+                    us = (v[0] + v[1]) + (v[2] + v[3]);
                     if constexpr (MODE == OUTM) {
-                        const int blk = tid >> 4;
+                        const int blk = i >> 4;
 #pragma unroll
-                        for (int q = 0; q <= RT; ++q) {
-                            const float v = s_m[(blk * (RT + 1) + q) * 16 + (tid & 15)];
-                            us += q <= blk ? v : -v;
+                        for (int q = part; q <= RT; q += NW) {
+                            const float *m = s_m + (blk * (RT + 1) + q) * 64 + (i & 15);
+                            us += q <= blk ? (m[0] + m[16]) + (m[32] + m[48]) : -m[0];
                         }
                     }
-                    a.u[static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p)] = us;
                 }
+                us = lanes_sum<NW>(us);
+                if (i < CT && part == 0 && inside(p, len))
+                    a.u[static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p)] = us;
             }
             // a wave finishes RTW row tiles from rt0 on
             const int rt0 = RTW * kp;
@@ -849,8 +873,13 @@ __global__ void __launch_bounds__(64 * NCW * KSP, 2) sweep_kernel(SweepArgs a) {
 }
 
 // The two state sweeps of the backward, and its three gradient sweeps, in one
-// launch each.  The sweeps of one segment and head read the same rows, so
-// they get neighbouring numbers on one XCD.
+// launch each.  The gradient sweeps go by groups of segments and heads, one
+// sweep after the other: most CUs then run the same instructions, and the
+// rows come from the caches the second and third time.  (All of one sweep
+// first: 5 % slower at 256 segments and heads of 1024 tokens; the three of a
+// segment next to each other: 20 % slower.)
+constexpr int SWEEP_GROUP = 128;
+
 struct Sweeps {
     SweepArgs s[3];
 };
@@ -867,9 +896,9 @@ template <class T, int DX, int NCW, bool VEC>
 __global__ void __launch_bounds__(64 * NCW, 2) gradient_kernel(Sweeps a) {
     extern __shared__ __align__(16) char smem[];
     constexpr bool B = sizeof(T) == 2;
-    const int64_t q = blockIdx.x >> 3, sh = (q / 3) * 8 + (blockIdx.x & 7);
+    const int64_t each = SWEEP_GROUP, in = blockIdx.x % (3 * each), sh = blockIdx.x / (3 * each) * each + in % each;
     if (sh >= a.s[0].segs * a.s[0].H) return;
-    switch (q % 3) {
+    switch (in / each) {
         case 0: sweep_body<T, DX, NCW, 1, 1, OUTM, B ? 2 : 1, B ? 3 : 1, B ? 3 : 1, VEC>(a.s[0], sh, smem); break;
         case 1: sweep_body<T, DX, NCW, 1, 1, OUTU, B ? 2 : 1, B ? 3 : 1, B ? 3 : 1, VEC>(a.s[1], sh, smem); break;
         default: sweep_body<T, DX, NCW, 1, 1, OUT, B ? 2 : 1, 1, B ? 2 : 1, VEC>(a.s[2], sh, smem); break;
@@ -896,6 +925,7 @@ struct Scans {
 };
 
 __global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
+    constexpr int AHEAD = 8;  // segments whose loads are in flight together
     const ScanArgs &a = two.s[blockIdx.y];
     const int64_t sh = blockIdx.x / a.blocks, n = sh / a.H;
     const int h = static_cast<int>(sh - n * a.H);
@@ -904,12 +934,22 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
     const int64_t s0 = a.pfx ? a.pfx[n] : n * a.nseg;
     const int cnt = a.pfx ? a.pfx[n + 1] - a.pfx[n] : a.nseg;
     float cur = a.init ? a.init[sh * a.dkv + e] : 0.f;
-    for (int i = 0; i < cnt; ++i) {
-        const int64_t sl = (s0 + (a.rev ? cnt - 1 - i : i)) * a.H + h;
-        float *p = a.tab + sl * a.dkv + e;
-        const float add = *p;
-        *p = cur;
-        cur = cur * __builtin_amdgcn_exp2f(static_cast<float>(a.tot[sl])) + add;
+    for (int i = 0; i < cnt; i += AHEAD) {
+        float *p[AHEAD], add[AHEAD], f[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {  // past the last: the last once more, not used
+            const int n = min(i + k, cnt - 1);
+            const int64_t sl = (s0 + (a.rev ? cnt - 1 - n : n)) * a.H + h;
+            p[k] = a.tab + sl * a.dkv + e;
+            add[k] = *p[k];
+            f[k] = __builtin_amdgcn_exp2f(static_cast<float>(a.tot[sl]));
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i + k < cnt) {
+                *p[k] = cur;
+                cur = cur * f[k] + add[k];
+            }
     }
     if (a.fin) {
         const int64_t lo = a.pfx ? a.seq[n].x : n * a.T;
@@ -933,8 +973,8 @@ struct DecayArgs {
     int H, nseg, L, la_tok;
 };
 
-__global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs a) {
-    __shared__ double red[4];
+__global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
+    __shared__ double red[16];
     const int64_t sh = blockIdx.x, seg = sh / a.H;
     const int h = static_cast<int>(sh - seg * a.H), tid = threadIdx.x, lane = tid & 63;
     if (a.pfx && seg >= a.pfx[a.N]) return;
@@ -963,46 +1003,54 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs a) {
     const float *s = last ? a.s_fin + (n * a.H + h) * a.dkv : a.s_tab + (sh + a.H) * a.dkv;
     const float *d = a.d_tab + sh * a.dkv;
     double x = 0.0;
-    for (int64_t e = tid; e < a.dkv; e += 256) x += static_cast<double>(s[e]) * d[e];
+    if (a.dkv % 4 == 0) {
+        for (int64_t e = 4 * tid; e < a.dkv; e += 4096) {
+            const float4 p = *reinterpret_cast<const float4 *>(s + e), q = *reinterpret_cast<const float4 *>(d + e);
+            x += (static_cast<double>(p.x) * q.x + static_cast<double>(p.y) * q.y) +
+                 (static_cast<double>(p.z) * q.z + static_cast<double>(p.w) * q.w);
+        }
+    } else {
+        for (int64_t e = tid; e < a.dkv; e += 1024) x += static_cast<double>(s[e]) * d[e];
+    }
+    auto total = [&](double v) {  // over the workgroup, the same on every lane
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
-    if (lane == 0) red[tid >> 6] = x;
-    __syncthreads();
-    x = red[0] + red[1] + red[2] + red[3];
+        for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+        __syncthreads();  // red's previous readers
+        if (lane == 0) red[tid >> 6] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) v += red[w];
+        return v;
+    };
+    x = total(x);
     // the reverse state has yet to pass the decay behind the segment
     if (!last) x *= exp(static_cast<double>(max(a.la[a.la_tok ? hi * a.H + h : h], LA_MIN)));
     double sum = 0.0;
     const float *uq = a.uq + static_cast<int64_t>(h) * a.tokens, *uk = a.uk + static_cast<int64_t>(h) * a.tokens;
-    for (int64_t top = hi; top > lo; top -= 1024) {  // tokens top-1-4 tid-j
-        double v[4];
-        const int64_t t0 = top - 1 - 4 * tid;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = t0 - j >= lo ? static_cast<double>(uq[t0 - j]) - static_cast<double>(uk[t0 - j]) : 0.0;
-#pragma unroll
-        for (int j = 1; j < 4; ++j) v[j] += v[j - 1];
-        const double upto = wave_prefix(v[3]);
-        __syncthreads();  // the previous round's readers
+    for (int64_t top = hi; top > lo; top -= 1024) {
+        const int64_t t = top - 1 - tid;
+        const double v = t >= lo ? static_cast<double>(uq[t]) - static_cast<double>(uk[t]) : 0.0;
+        const double upto = wave_prefix(v);
+        __syncthreads();  // red's previous readers
         if (lane == 63) red[tid >> 6] = upto;
         __syncthreads();
-        double before = upto - v[3];
+        double before = 0.0, all = 0.0;
 #pragma unroll
-        for (int w = 0; w < 3; ++w) before += w < (tid >> 6) ? red[w] : 0.0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (t0 - j >= lo) {
-                const double g = x + before + v[j];
-                if (a.la_tok) a.d_la[(t0 - j) * a.H + h] = static_cast<float>(g);
-                sum += g;
-            }
-        x += red[0] + red[1] + red[2] + red[3];
+        for (int w = 0; w < 16; ++w) {
+            before += w < (tid >> 6) ? red[w] : 0.0;
+            all += red[w];
+        }
+        if (t >= lo) {
+            const double g = x + before + upto;
+            if (a.la_tok) a.d_la[t * a.H + h] = static_cast<float>(g);
+            sum += g;
+        }
+        x += all;
     }
     if (!a.la_tok) {
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-        __syncthreads();
-        if (lane == 0) red[tid >> 6] = sum;
-        __syncthreads();
-        if (tid == 0) a.part[sh] = red[0] + red[1] + red[2] + red[3];
+        sum = total(sum);
+        if (tid == 0) a.part[sh] = sum;
     }
 }
 
@@ -1176,7 +1224,7 @@ template <class T, int D, bool VEC>
 hipError_t launch_gradients(const Sweeps &a, hipStream_t s) {
     constexpr int NCW = D / 16;
     using Sh = Shape<T, D, NCW, 1, 1>;
-    const int64_t groups = (a.s[0].segs * a.s[0].H + 7) / 8 * 8;
+    const int64_t groups = (a.s[0].segs * a.s[0].H + SWEEP_GROUP - 1) / SWEEP_GROUP * SWEEP_GROUP;
     return launch_lds(gradient_kernel<T, D, NCW, VEC>, 3 * groups, 64 * NCW, Sh::bytes(OUTM, sizeof(T) == 2 ? 2 : 1), a, s);
 }
 template <class T, int D>
@@ -1345,7 +1393,7 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
                    l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,
                    base.nseg, c.L, l.la_tok};
     if (c.segs * l.H > 0) {
-        hipLaunchKernelGGL(decay_grad_kernel, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(256), 0, s, d);
+        hipLaunchKernelGGL(decay_grad_kernel, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(1024), 0, s, d);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!l.la_tok) {
