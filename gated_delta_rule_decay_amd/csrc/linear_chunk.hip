@@ -924,23 +924,31 @@ struct Scans {
     ScanArgs s[2];
 };
 
+// V elements of the state a lane (V = 4: whole 16-byte units).
+template <int V>
 __global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
     constexpr int AHEAD = 8;  // segments whose loads are in flight together
+    typedef float Fv __attribute__((ext_vector_type(V)));
     const ScanArgs &a = two.s[blockIdx.y];
     const int64_t sh = blockIdx.x / a.blocks, n = sh / a.H;
     const int h = static_cast<int>(sh - n * a.H);
-    const int64_t e = static_cast<int64_t>(blockIdx.x % a.blocks) * 256 + threadIdx.x;
+    const int64_t e = (static_cast<int64_t>(blockIdx.x % a.blocks) * 256 + threadIdx.x) * V;
     if (e >= a.dkv) return;
     const int64_t s0 = a.pfx ? a.pfx[n] : n * a.nseg;
     const int cnt = a.pfx ? a.pfx[n + 1] - a.pfx[n] : a.nseg;
-    float cur = a.init ? a.init[sh * a.dkv + e] : 0.f;
+    auto at = [&](const float *p) { return reinterpret_cast<const Fv *>(p); };
+    Fv cur = 0.f;
+    if (a.init)
+#pragma unroll
+        for (int k = 0; k < V; ++k) cur[k] = a.init[sh * a.dkv + e + k];  // a caller's state: any alignment
     for (int i = 0; i < cnt; i += AHEAD) {
-        float *p[AHEAD], add[AHEAD], f[AHEAD];
+        Fv *p[AHEAD], add[AHEAD];
+        float f[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {  // past the last: the last once more, not used
-            const int n = min(i + k, cnt - 1);
-            const int64_t sl = (s0 + (a.rev ? cnt - 1 - n : n)) * a.H + h;
-            p[k] = a.tab + sl * a.dkv + e;
+            const int m = min(i + k, cnt - 1);
+            const int64_t sl = (s0 + (a.rev ? cnt - 1 - m : m)) * a.H + h;
+            p[k] = const_cast<Fv *>(at(a.tab + sl * a.dkv + e));
             add[k] = *p[k];
             f[k] = __builtin_amdgcn_exp2f(static_cast<float>(a.tot[sl]));
         }
@@ -954,7 +962,8 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
     if (a.fin) {
         const int64_t lo = a.pfx ? a.seq[n].x : n * a.T;
         if (a.rev && cnt > 0) cur *= __expf(a.la[a.la_tok ? lo * a.H + h : h]);
-        a.fin[sh * a.dkv + e] = cur;
+#pragma unroll
+        for (int k = 0; k < V; ++k) a.fin[sh * a.dkv + e + k] = cur[k];
     }
 }
 
@@ -1066,9 +1075,71 @@ __global__ void __launch_bounds__(64) decay_sum_kernel(const double *part, const
     if (lane == 0) d_la[h] = static_cast<float>(s);
 }
 
+// The plan of up to 1024 packed sequences in one launch (the two of
+// varlen.hip else): every workgroup counts the segments of all sequences and
+// fills its share of the segment table.
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int n, int64_t T, int L, int cap, int2 *seq, int *pfx,
+                                                   int2 *tab) {
+    __shared__ int64_t part[16];
+    __shared__ int first[1025], from[1024], to[1024];
+    const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+    int64_t lo = 0, hi = 0, sum = 0;
+    if (i < n) {
+        lo = min(max(static_cast<int64_t>(cu[i]), int64_t(0)), T);
+        hi = min(max(static_cast<int64_t>(cu[i + 1]), lo), T);
+        sum = (hi - lo + L - 1) / L;
+        from[i] = static_cast<int>(lo);
+        to[i] = static_cast<int>(hi);
+    }
+    const int64_t mine = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t x = __shfl_up(sum, o);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 63) part[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) sum += part[w];
+    if (i < n) {
+        first[i] = static_cast<int>(min(sum - mine, static_cast<int64_t>(cap)));
+        if (i == n - 1) first[n] = static_cast<int>(min(sum, static_cast<int64_t>(cap)));
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        if (i < n) {
+            seq[i] = make_int2(from[i], to[i]);
+            pfx[i] = first[i];
+        }
+        if (i == 0) pfx[n] = first[n];
+    }
+    const int total = first[n];
+    for (int s = blockIdx.x * 1024 + i; s < total; s += gridDim.x * 1024) {
+        int l = 0, r = n - 1;  // the last sequence that starts at or before segment s
+        while (l < r) {
+            const int mid = (l + r + 1) >> 1;
+            if (first[mid] <= s) l = mid;
+            else r = mid - 1;
+        }
+        tab[s] = make_int2(from[l] + L * (s - first[l]), to[l]);
+    }
+}
+
 // ---- host side
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
+
+hipError_t launch_plan(const LinArgs &a, int L, char *buf, VarPlan *plan, hipStream_t s) {
+    if (a.N > 1024) return launch_varlen_plan(a.cu, a.N, a.T, L, buf, plan, s);
+    const int n = static_cast<int>(a.N);
+    int2 *seq = reinterpret_cast<int2 *>(buf);
+    int *pfx = reinterpret_cast<int *>(buf + align256(a.N * 8));
+    int2 *tab = reinterpret_cast<int2 *>(buf + align256(a.N * 8) + align256((a.N + 1) * 4));
+    const int64_t cap = varlen_chunk_bound(a.N, a.T, L), blocks = (cap + 1023) / 1024;
+    hipLaunchKernelGGL(plan_kernel, dim3(static_cast<unsigned>(blocks < 256 ? blocks : 256)), dim3(1024), 0, s, a.cu, n, a.T, L,
+                       static_cast<int>(cap), seq, pfx, tab);
+    *plan = VarPlan{seq, pfx, tab};
+    return hipGetLastError();
+}
 
 struct Cut {
     int L;         // tokens of a segment
@@ -1088,8 +1159,10 @@ Cut cut_of(const LinArgs &a, int64_t L) {
 Cut fwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
     if (a.T <= 256 || heads >= 128) return Cut{0, 1, a.N};
-    int64_t L = (a.T * heads / 512 + 63) / 64 * 64;
-    if (L < 128) L = 128;
+    // whole chunks, and two segments or more for each CU
+    const int64_t C = a.bf16 ? 64 : 32;
+    int64_t L = (a.T * heads / 512 + C - 1) / C * C;
+    if (L < 96) L = a.bf16 ? 128 : 96;
     if (!a.cu && L >= a.T) return Cut{0, 1, a.N};
     return cut_of(a, L);
 }
@@ -1098,7 +1171,7 @@ Cut fwd_cut(const LinArgs &a) {
 // which bounds how far the differences of the decay's gradient are summed.
 Cut bwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
-    int64_t L = (a.T * heads / (a.dk > 64 || a.dv > 64 ? 256 : 768) + 63) / 64 * 64;
+    int64_t L = (a.T * heads / (a.dk > 64 || a.dv > 64 ? 256 : 512) + 63) / 64 * 64;
     if (L < 64) L = 64;
     if (L > 1024) L = 1024;
     return cut_of(a, L);
@@ -1190,11 +1263,15 @@ int granularity(const LinArgs &l, int64_t d, std::initializer_list<const void *>
 }
 
 hipError_t launch_scans(Scans a, int n, hipStream_t s) {
-    for (int i = 0; i < n; ++i) a.s[i].blocks = static_cast<int>((a.s[i].dkv + 255) / 256);
+    const int v = a.s[0].dkv % 4 == 0 ? 4 : 1;
+    for (int i = 0; i < n; ++i) a.s[i].blocks = static_cast<int>((a.s[i].dkv + 256 * v - 1) / (256 * v));
     const int64_t grid = a.s[0].N * a.s[0].H * a.s[0].blocks;
     if (grid <= 0) return hipSuccess;
     if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(segment_scan_kernel, dim3(static_cast<unsigned>(grid), n), dim3(256), 0, s, a);
+    if (v == 4)
+        hipLaunchKernelGGL(segment_scan_kernel<4>, dim3(static_cast<unsigned>(grid), n), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(segment_scan_kernel<1>, dim3(static_cast<unsigned>(grid), n), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1302,7 +1379,7 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
     VarPlan vp;
     const FwdSpace f = fwd_space(l, c, ws);
     const bool cut = c.L > 0;
-    if (cut && l.cu && (e = launch_varlen_plan(l.cu, l.N, l.T, c.L, f.plan, &vp, s)) != hipSuccess) return e;
+    if (cut && l.cu && (e = launch_plan(l, c.L, f.plan, &vp, s)) != hipSuccess) return e;
     SweepArgs a = sweep_of(l, c, cut && l.cu ? &vp : nullptr);
     a.x = l.q;
     a.y = l.k;
@@ -1338,7 +1415,7 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     const BwdSpace f = bwd_space(l, c, ws);
     hipError_t e;
     VarPlan vp;
-    if (l.cu && (e = launch_varlen_plan(l.cu, l.N, l.T, c.L, f.plan, &vp, s)) != hipSuccess) return e;
+    if (l.cu && (e = launch_plan(l, c.L, f.plan, &vp, s)) != hipSuccess) return e;
     SweepArgs base = sweep_of(l, c, l.cu ? &vp : nullptr);
     base.ncb = 1;
     const int dk = static_cast<int>(l.dk), dv = static_cast<int>(l.dv);
