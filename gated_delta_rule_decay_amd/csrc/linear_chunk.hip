@@ -50,7 +50,7 @@ struct SweepArgs {
     const void *x, *y, *z;   // rows [token, H, dx], [token, H, dx], [token, H, dz]
     void *out;               // rows [token, H, dz]
     const void *w;           // rows [token, H, dz], for u
-    float *u;                // [H][tokens]
+    float *u, *m;            // [H][tokens]: per token what it adds to the decay's gradient (OUTU, OUTM)
     const float *la;
     const float *s_in;       // [segment][H][dk*dv] or nullptr (zeros)
     float *s_out;            // the same, or nullptr
@@ -397,12 +397,12 @@ struct Shape {
 // them, the state to NS, the decayed values that update the state to NU (three
 // parts hold all 24 bits; fp32 inputs are not split).
 //
-// OUTU and OUTM (all of z's columns in one workgroup): per token the part of
-// the decay's gradient that it opens or closes,
-//   u_i = <w_i, e^{g_i} S^T x_i>  [+ sum_{j<i} M_ij - sum_{j>i} M_ji],
+// OUTU and OUTM (all of z's columns in one workgroup): per token what it adds
+// to the decay's gradient, through the state and (OUTM) inside its chunk,
+//   u_i = <w_i, e^{g_i} S^T x_i>,   m_i = sum_{j<i} M_ij - sum_{j>i} M_ji,
 //   M_ij = (score i, j) (w_i . z_j):
-// pairs inside a chunk enter both their ends with the same fp32 value, so the
-// sum over a chunk's tail keeps their precision.
+// a pair inside a chunk enters both its ends with the same fp32 value, so the
+// sum of m over a chunk's tail keeps its precision.
 template <class T, int DX, int NCW, int NT, int KSP, int MODE, int NP, int NS, int NU, bool VEC>
 __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, char *smem) {
     using E = Elem<T>;
@@ -743,7 +743,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
         if constexpr (MODE != STATE) {
             if constexpr (MODE >= OUTU) {  // NW neighbouring lanes a token
                 const int i = tid / NW, part = tid % NW, p = p0 + i;
-                float us = 0.f;
+                float us = 0.f, ms = 0.f;
                 if (i < CT) {
                     const f32x4 v = *reinterpret_cast<const f32x4 *>(s_u + (part * CT + i) * 4);
                     us = (v[0] + v[1]) + (v[2] + v[3]);
@@ -752,13 +752,17 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 #pragma unroll
                         for (int q = part; q <= RT; q += NW) {
                             const float *m = s_m + (blk * (RT + 1) + q) * 64 + (i & 15);
-                            us += q <= blk ? (m[0] + m[16]) + (m[32] + m[48]) : -m[0];
+                            ms += q <= blk ? (m[0] + m[16]) + (m[32] + m[48]) : -m[0];
                         }
                     }
                 }
                 us = lanes_sum<NW>(us);
-                if (i < CT && part == 0 && inside(p, len))
-                    a.u[static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p)] = us;
+                if constexpr (MODE == OUTM) ms = lanes_sum<NW>(ms);
+                if (i < CT && part == 0 && inside(p, len)) {
+                    const int64_t at = static_cast<int64_t>(h) * a.tokens + (rev ? first - p : first + p);
+                    a.u[at] = us;
+                    if constexpr (MODE == OUTM) a.m[at] = ms;
+                }
             }
             // a wave finishes RTW row tiles from rt0 on
             const int rt0 = RTW * kp;
@@ -967,10 +971,11 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
     }
 }
 
-// d la of a segment: its last token's <S, dS>, then back over the segment the
-// differences of the row products, in 64 bits.  One workgroup per (segment, head).
+// d la of a segment: its last token's <S, dS>, then back over the segment what
+// its tokens open and close of the state's part, and over each chunk its pairs;
+// in 64 bits, a wave on the 64 tokens of a chunk (or two chunks of 32).  One workgroup per (segment, head).
 struct DecayArgs {
-    const float *uq, *uk;   // [H][tokens]
+    const float *uq, *uk, *m;  // [H][tokens]
     const float *s_tab, *d_tab;  // states entering the segments, forward and reverse
     const float *s_fin;     // [N][H][dk*dv] final states
     const float *la;
@@ -979,7 +984,7 @@ struct DecayArgs {
     const int2 *tab, *seq;
     const int *pfx;
     int64_t N, T, tokens, segs, dkv;
-    int H, nseg, L, la_tok;
+    int H, nseg, L, la_tok, half;  // half: chunks of 32 tokens, not 64
 };
 
 __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
@@ -1037,10 +1042,16 @@ __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
     if (!last) x *= exp(static_cast<double>(max(a.la[a.la_tok ? hi * a.H + h : h], LA_MIN)));
     double sum = 0.0;
     const float *uq = a.uq + static_cast<int64_t>(h) * a.tokens, *uk = a.uk + static_cast<int64_t>(h) * a.tokens;
-    for (int64_t top = hi; top > lo; top -= 1024) {
+    const float *um = a.m + static_cast<int64_t>(h) * a.tokens;
+    for (int64_t top = lo + (hi - lo + 63) / 64 * 64; top > lo; top -= 1024) {
         const int64_t t = top - 1 - tid;
-        const double v = t >= lo ? static_cast<double>(uq[t]) - static_cast<double>(uk[t]) : 0.0;
-        const double upto = wave_prefix(v);
+        const bool live = t >= lo && t < hi;
+        const double upto = wave_prefix(live ? static_cast<double>(uq[t]) - static_cast<double>(uk[t]) : 0.0);
+        double pairs = wave_prefix(live ? static_cast<double>(um[t]) : 0.0);
+        if (a.half) {
+            const double first = __shfl(pairs, 31);
+            if (lane >= 32) pairs -= first;
+        }
         __syncthreads();  // red's previous readers
         if (lane == 63) red[tid >> 6] = upto;
         __syncthreads();
@@ -1050,8 +1061,8 @@ __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
             before += w < (tid >> 6) ? red[w] : 0.0;
             all += red[w];
         }
-        if (t >= lo) {
-            const double g = x + before + upto;
+        if (live) {
+            const double g = x + before + upto + pairs;
             if (a.la_tok) a.d_la[t * a.H + h] = static_cast<float>(g);
             sum += g;
         }
@@ -1345,7 +1356,7 @@ FwdSpace fwd_space(const LinArgs &a, const Cut &c, void *ws) {
 }
 
 struct BwdSpace {
-    float *s_tab, *d_tab, *s_fin, *uq, *uk;
+    float *s_tab, *d_tab, *s_fin, *uq, *uk, *um;
     double *s_tot, *d_tot, *part;
     char *plan;
     int64_t bytes;
@@ -1363,6 +1374,7 @@ BwdSpace bwd_space(const LinArgs &a, const Cut &c, void *ws) {
     f.part = b.take<double>(c.segs * a.H);
     f.uq = b.take<float>(a.H * tokens);
     f.uk = b.take<float>(a.H * tokens);
+    f.um = b.take<float>(a.H * tokens);
     if (a.cu) f.plan = b.take<char>(static_cast<int64_t>(varlen_plan_bytes(a.N, a.T, c.L)));
     f.bytes = b.used;
     return f;
@@ -1447,7 +1459,7 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     q.x = l.d_o; q.y = l.v; q.z = l.k; q.dx = dv; q.dz = dk; q.gx = gv; q.gz = gk;
     q.s_t = 1;
     k = q;
-    q.out = l.dq; q.w = l.q; q.u = f.uq;
+    q.out = l.dq; q.w = l.q; q.u = f.uq; q.m = f.um;
     q.s_in = f.s_tab;
     q.p_scale = q.s_scale = l.scale;
     k.x = l.v; k.y = l.d_o; k.z = l.q;
@@ -1466,9 +1478,9 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
         if ((e = launch_typed<OUT, 2, 1, 2>(l, v, TALL, vec, s)) != hipSuccess) return e;
     }
 
-    DecayArgs d = {f.uq, f.uk, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,
+    DecayArgs d = {f.uq, f.uk, f.um, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,
                    l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,
-                   base.nseg, c.L, l.la_tok};
+                   base.nseg, c.L, l.la_tok, !l.bf16};
     if (c.segs * l.H > 0) {
         hipLaunchKernelGGL(decay_grad_kernel, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(1024), 0, s, d);
         if ((e = hipGetLastError()) != hipSuccess) return e;
