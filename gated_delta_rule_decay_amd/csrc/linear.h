@@ -28,6 +28,8 @@ struct LinArgs {
     float *d_s0;            // [N,H,dk,dv] or nullptr
 };
 
+// whether every launch of a request stays below 2^32 lanes
+bool linear_fits(const LinArgs &a, bool backward);
 size_t linear_fwd_workspace(const LinArgs &a);
 size_t linear_bwd_workspace(const LinArgs &a);
 hipError_t launch_linear_fwd(const LinArgs &a, void *ws, hipStream_t s);  // ws nullptr: one pass

@@ -69,11 +69,8 @@ gdn2_status check_linear(const gdn2_linear_desc *d, bool packed) {
     if (!product_ok({packed ? 1 : d->batch, d->seqlen, d->heads, dmax, 16}) ||
         !product_ok({d->batch, d->heads, d->dk, d->dv, 16}))
         return GDN2_ERR_SHAPE;
-    // launch sizes: 64 workgroups a state, three a segment of 64 tokens
-    const int64_t chains = d->batch * d->heads, rows = (packed ? 1 : d->batch) * d->heads, segs = d->seqlen / 64 + 1;
-    if (d->seqlen > INT32_MAX || chains > (INT32_MAX >> 6) || d->heads > 65535 ||  // 32-bit offsets inside a chunk
-        rows > (INT64_C(1) << 40) / segs || 3 * (rows * segs + chains + 8) > INT32_MAX)
-        return GDN2_ERR_UNSUPPORTED;
+    // 32-bit offsets inside a chunk, 2^32 lanes a launch over the chains
+    if (d->seqlen > INT32_MAX || d->heads > 65535 || d->batch * d->heads >= (INT64_C(1) << 20)) return GDN2_ERR_UNSUPPORTED;
     return GDN2_OK;
 }
 
@@ -110,6 +107,7 @@ gdn2_status space_of(const gdn2_linear_desc *d, bool packed, bool backward, size
     const gdn2_status st = check_linear(d, packed);
     if (st != GDN2_OK) return st;
     const LinArgs a = args_of(d, packed ? &packed_mark : nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+    if (!gdn2::linear_fits(a, backward)) return GDN2_ERR_UNSUPPORTED;
     *bytes = backward ? gdn2::linear_bwd_workspace(a) : gdn2::linear_fwd_workspace(a);
     return GDN2_OK;
 }
@@ -178,8 +176,8 @@ gdn2_status check_norm(const gdn2_norm_desc *d) {
         return GDN2_ERR_DTYPE;
     if (!(d->eps >= 0.f)) return GDN2_ERR_SHAPE;
     if (!product_ok({d->rows, d->dim, 16})) return GDN2_ERR_SHAPE;
-    if (d->dim > 16384 || d->rows > INT32_MAX || !product_ok({d->groups, d->dim, 8}) ||
-        d->groups > INT32_MAX / ((d->dim + 15) / 16))
+    // 2^32 lanes a launch: 1024 for 16 columns of a weight row
+    if (d->dim > 16384 || d->rows > INT32_MAX || d->groups >= (INT64_C(1) << 22) / ((d->dim + 15) / 16))
         return GDN2_ERR_UNSUPPORTED;
     return GDN2_OK;
 }

@@ -1382,6 +1382,14 @@ BwdSpace bwd_space(const LinArgs &a, const Cut &c, void *ws) {
 
 }  // namespace
 
+bool linear_fits(const LinArgs &a, bool backward) {
+    const Cut c = backward ? bwd_cut(a) : fwd_cut(a);
+    // workgroups of up to 1024 lanes a segment and head, three of 512 in the
+    // gradient sweeps; 16 of 256 a state
+    const int64_t most = INT64_C(1) << 32, sh = c.segs * a.H + SWEEP_GROUP;
+    return sh < most / (backward ? 1536 : 1024) && a.N * a.H < most / 4096;
+}
+
 size_t linear_fwd_workspace(const LinArgs &a) { return static_cast<size_t>(fwd_space(a, fwd_cut(a), nullptr).bytes); }
 size_t linear_bwd_workspace(const LinArgs &a) { return static_cast<size_t>(bwd_space(a, bwd_cut(a), nullptr).bytes); }
 

@@ -219,3 +219,36 @@ def test_layer_of_mixer_and_norm(g):
         snap = {n: t.clone() for n, t in kept.items()}
         for n, t in layer().items():
             assert torch.equal(snap[n], t), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape,heads", [((2300, 16, 128), True), ((9000, 512), False), ((1300, 4096), False), ((5000, 33), False),
+                                        ((700, 10000), False)])
+def test_many_rounds(g, shape, heads, dtype):
+    # more rows than one round of the launch takes
+    check_all(g, *make(shape, dtype, shape[-2:] if heads else shape[-1:], F32, seed=3))
+
+
+def test_bad_rows_stay_alone(g):
+    x, w, b, dy = gpu(*make((40, 3, 72), BF, (3, 72), F32))
+    one = g.layer_norm_fwd(x, w, b)
+    grads = g.layer_norm_bwd(dy, x, w, one[1], one[2], want_bias=True)
+    x2, dy2 = x.clone(), dy.clone()
+    x2[0, 1], dy2[0, 1] = float("nan"), float("inf")
+    two = g.layer_norm_fwd(x2, w, b)
+    grads2 = g.layer_norm_bwd(dy2, x2, w, two[1], two[2], want_bias=True)
+    keep = torch.ones(40, 3, dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    for p, q in zip(one, two):
+        assert torch.equal(p[keep], q[keep])
+    assert torch.equal(grads[0][keep], grads2[0][keep])
+    for p, q in zip(grads[1:], grads2[1:]):  # the other heads' weights
+        assert torch.equal(p[[0, 2]], q[[0, 2]])
+
+
+def test_outputs_stay_inside_their_tensors(g):
+    for D in (33, 64, 8200):
+        x, w, b, dy = gpu(*make((5, D), BF, (D,), F32))
+        big = torch.full((5 * D + 64,), 9.0, dtype=BF, device="cuda")
+        g.layer_norm_fwd(x, w, b, out=big[32:-32].view(5, D))
+        assert (big[:32] == 9).all() and (big[-32:] == 9).all()

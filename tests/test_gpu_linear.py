@@ -59,7 +59,7 @@ def run_forward(g, d, scale, dtype, **kw):
     return o, S
 
 
-HEADS = [(128, 128), (64, 64), (72, 56), (1, 1), (33, 100), (128, 17), (5, 128), (65, 64), (40, 128)]
+HEADS = [(128, 128), (64, 64), (72, 56), (1, 1), (33, 100), (128, 17), (5, 128), (65, 64), (40, 128), (66, 70), (127, 127)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -220,7 +220,7 @@ def test_packed_bad_offsets_stay_inside(g, offsets):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (72, 56), (1, 1), (33, 100), (128, 17), (17, 128)])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (72, 56), (1, 1), (33, 100), (128, 17), (17, 128), (66, 70), (126, 102)])
 @pytest.mark.parametrize("T", [1, 65, 300])
 def test_backward(g, T, dk, dv, dtype):
     d = make(2, T, 2, dk, dv, dtype, seed=T)
@@ -372,3 +372,107 @@ def test_two_streams(g):
     torch.cuda.synchronize()
     for (o, S), (o2, S2) in zip(got, want):
         assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+# where the launch chooses: segments below 128 chains, halves of heads from
+# 128, whole heads from 256; one head more or less on each side
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H", [(1, 127), (1, 128), (51, 5), (16, 16)])
+def test_forward_many_chains(g, B, H, dtype):
+    d = make(B, 260, H, 72, 80, dtype, seed=H)
+    o_ref, S_ref = ref.linear_forward(d["q"], d["k"], d["v"], d["la"], d["s0"], 0.4)
+    o, S = run_forward(g, d, 0.4, dtype)
+    ref.check("o", o, o_ref, ref.TWO if dtype == BF else ref.F32, bound_o(d, o_ref, 0.4, dtype, 260))
+    ref.check("state", S, S_ref, ref.F32)
+
+
+def test_packed_many_heads(g):
+    # whole sequences, one workgroup each: an empty one among them
+    lens, H = [70, 0, 1, 300], 130
+    d = make(4, sum(lens), H, 32, 48, BF, packed=True)
+    x = dev(d)
+    cu = torch.tensor([0, 70, 70, 71, 371], dtype=torch.int32, device="cuda")
+    o, S = g.linear_chunk_fwd_varlen(x["q"], x["k"], x["v"], x["la"], cu, x["s0"])
+    for i, at, n, s in split(d, lens, H):
+        o_ref, S_ref = ref.linear_forward(s["q"], s["k"], s["v"], s["la"], s["s0"], 1.0)
+        if n:
+            ref.check(f"o {i}", o[at:at + n][None], o_ref, ref.TWO, bound_o(s, o_ref, 1.0, BF, n))
+        ref.check(f"state {i}", S[i:i + 1], S_ref, ref.F32)
+
+
+def test_packed_many_sequences(g):
+    # over 1024 sequences: the plan's other form
+    N, H = 1500, 2
+    lens = [(7 * i) % 5 for i in range(N)]
+    offs = [0]
+    for n in lens:
+        offs.append(offs[-1] + n)
+    d = make(N, offs[-1], H, 16, 24, BF, packed=True)
+    x = dev(d)
+    cu = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    o, S = g.linear_chunk_fwd_varlen(x["q"], x["k"], x["v"], x["la"], cu, x["s0"])
+    gr = g.linear_chunk_bwd_varlen(x["q"], x["k"], x["v"], x["la"], cu, x["s0"], x["d_o"], x["d_s"])
+    # the same sequences as a padded batch: no decay and no key behind an end
+    pad = lambda t: torch.stack([torch.cat([t[a:b], t.new_zeros((4 - (b - a), *t.shape[1:]))]) for a, b in zip(offs, offs[1:])])
+    args = [pad(d[n]) for n in ("q", "k", "v", "la")]
+    o_ref, S_ref = ref.linear_forward(*args, d["s0"], 1.0)
+    b = ref.linear_backward(*args, d["s0"], 1.0, pad(d["d_o"]), d["d_s"])
+    take = lambda t: torch.cat([t[i, :n] for i, n in enumerate(lens)])
+    ref.check("o", o, take(o_ref), ref.TWO)
+    ref.check("state", S, S_ref, ref.F32)
+    for n in ("dq", "dk", "dv", "d_log_decay"):
+        ref.check(n, gr[n], take(b[n]), ref.F32 if n == "d_log_decay" else ref.TWO if n == "dv" else ref.ONE)
+    ref.check("d_state0", gr["d_state0"], b["d_state0"], ref.F32)
+
+
+def test_packed_neighbours_do_not_mix(g):
+    # one sequence of NaN, and NaN behind the last one
+    lens, H = [65, 70, 130], 2
+    d = dev(make(3, sum(lens) + 9, H, 64, 64, BF, packed=True))
+    cu = torch.tensor([0, 65, 135, 265], dtype=torch.int32, device="cuda")
+    run = lambda: (g.linear_chunk_fwd_varlen(d["q"], d["k"], d["v"], d["la"], cu, d["s0"]),
+                   g.linear_chunk_bwd_varlen(d["q"], d["k"], d["v"], d["la"], cu, d["s0"], d["d_o"], d["d_s"]))
+    (o1, S1), g1 = run()
+    for n in ("q", "k", "v", "d_o"):
+        d[n][65:135] = float("nan")
+        d[n][265:] = float("nan")
+    (o2, S2), g2 = run()
+    keep = torch.cat([torch.arange(65), torch.arange(135, 265)]).cuda()
+    assert torch.equal(o1[keep], o2[keep]) and torch.equal(S1[[0, 2]], S2[[0, 2]])
+    for n in ("dq", "dk", "dv", "d_log_decay"):
+        assert torch.equal(g1[n][keep], g2[n][keep]), n
+    assert torch.equal(g1["d_state0"][[0, 2]], g2["d_state0"][[0, 2]])
+
+
+def test_outputs_stay_inside_their_tensors(g):
+    # borders of the outputs, at head sizes whose rows end inside a unit
+    for dtype, dk, dv in ((BF, 66, 33), (F32, 33, 70), (BF, 128, 127)):
+        d = dev(make(1, 75, 3, dk, dv, dtype))
+        big = torch.full((75 * 3 * dv + 64,), 9.0, dtype=dtype, device="cuda")
+        st = torch.full((3 * dk * dv + 64,), 9.0, device="cuda")
+        g.linear_chunk_fwd(d["q"], d["k"], d["v"], d["la"], d["s0"], out=big[32:-32].view(1, 75, 3, dv),
+                           state_out=st[32:-32].view(1, 3, dk, dv))
+        for x in (big, st):
+            assert (x[:32] == 9).all() and (x[-32:] == 9).all()
+        step = torch.full((3 * dv + 64,), 9.0, dtype=dtype, device="cuda")
+        g.linear_recurrent_step(d["q"][:, 0].contiguous(), d["k"][:, 0].contiguous(), d["v"][:, 0].contiguous(),
+                                d["la"][:, 0].contiguous(), d["s0"], out=step[32:-32].view(1, 3, dv))
+        assert (step[:32] == 9).all() and (step[-32:] == 9).all()
+
+
+def test_two_graphs_with_workspaces_of_their_own(g):
+    d = dev(make(1, 500, 2, 128, 64, BF))
+    want = g.linear_chunk_bwd(d["q"], d["k"], d["v"], d["la"], d["s0"], d["d_o"], d["d_s"])
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(g.linear_chunk_bwd(d["q"], d["k"], d["v"], d["la"], d["s0"], d["d_o"], d["d_s"]))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            for n in want:
+                assert torch.equal(o[n], want[n]), n
