@@ -19,8 +19,18 @@
 // So one kernel, the sweep over rows (x, y, z) = (query, key, value) roles,
 // serves the forward and the backward.  The decay's gradient follows from
 //   d la_t = <S_e, dS_e> + sum_{t<=i<=e} (q_i . dq_i - k_i . dk_i)
-// for any e >= t of the sequence: the sweeps of dq and dk also store the row
-// products q.dq and k.dk, taken from their fp32 accumulators.
+// for any e >= t of the sequence.  The part of each product that a pair of
+// tokens in one chunk adds is in both terms, so it is formed once, in the
+// sweep of dq, and summed over the chunk alone; the rest, what the state adds,
+// is stored per token by the sweeps of dq and dk in fp32, and summed in 64
+// bits over a segment from the <S, dS> of its end.
+//
+// Bound by HBM (the forward reads q, k, v and writes o: 4 dk dv operations
+// for 2 (2 dk + 2 dv) bytes a token and head, a quarter of what a large
+// product reaches).  Measured, H=16, d=128, bf16, decays and an initial state:
+// 8 x 4096 tokens 193-203 us (2.9 TB/s; a large copy takes 113), 65536 tokens
+// 380 us (k and v read twice: 4.2 TB/s), the backward of 4 x 4096 tokens
+// 390-400 us.
 //
 // Long sequences are cut into segments: a state-only sweep forms what every
 // segment adds to the state, a scan over the segments turns these into the
@@ -1166,13 +1176,21 @@ Cut cut_of(const LinArgs &a, int64_t L) {
     return c;
 }
 
-// Forward: segments only where whole chains leave the chip empty.
+// Tokens of a segment, in whole chunks, so that all heads together have at
+// most `most` of them (packed sequences: and one more each).
+int64_t segment_tokens(const LinArgs &a, int64_t most) {
+    const int64_t heads = a.H * (a.cu || a.N < 1 ? 1 : a.N), n = heads < most ? most / heads : 1, C = a.bf16 ? 64 : 32;
+    return ((a.T + n - 1) / n + C - 1) / C * C;
+}
+
+// Forward: segments where whole chains leave the chip empty, two for each CU.
+// Measured (H=16, d=128, bf16), whole chains and segments: 64 chains of 4096
+// tokens 185 and 114 us, 128 chains 193 and 214; 16 chains of 512 tokens 28
+// and 30 us, of 1024 49 and 34 (fp32, 256 tokens: 38 and 45; 512: 68 and 49).
 Cut fwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
-    if (a.T <= 256 || heads >= 128) return Cut{0, 1, a.N};
-    // whole chunks, and two segments or more for each CU
-    const int64_t C = a.bf16 ? 64 : 32;
-    int64_t L = (a.T * heads / 512 + C - 1) / C * C;
+    if (a.T <= (a.bf16 ? 512 : 256) || heads >= 112) return Cut{0, 1, a.N};
+    int64_t L = segment_tokens(a, 512);
     if (L < 96) L = a.bf16 ? 128 : 96;
     if (!a.cu && L >= a.T) return Cut{0, 1, a.N};
     return cut_of(a, L);
@@ -1180,12 +1198,11 @@ Cut fwd_cut(const LinArgs &a) {
 
 // Backward: always through the segments' states, at most 1024 tokens apart,
 // which bounds how far the differences of the decay's gradient are summed.
+// One gradient sweep of eight waves fills a CU (2048 or 512 tokens at 64
+// chains: 7 and 12 % slower), or two of four waves.
 Cut bwd_cut(const LinArgs &a) {
-    const int64_t heads = a.H * (a.cu ? 1 : a.N);
-    int64_t L = (a.T * heads / (a.dk > 64 || a.dv > 64 ? 256 : 512) + 63) / 64 * 64;
-    if (L < 64) L = 64;
-    if (L > 1024) L = 1024;
-    return cut_of(a, L);
+    const int64_t L = segment_tokens(a, a.dk > 64 || a.dv > 64 ? 256 : 512);
+    return cut_of(a, L < 64 ? 64 : L > 1024 ? 1024 : L);
 }
 
 template <class T, int DX, int NCW, int NT, int KSP, int MODE, int NP, int NS, int NU>
@@ -1216,13 +1233,17 @@ hipError_t launch_shape(SweepArgs a, bool vec, hipStream_t s) {
 //          sweeps that hold more operands
 //   SPLIT  64 columns, four pairs of waves, each pair sharing 16 columns and
 //          taking half of the channels: eight waves on half of a head, where
-//          heads are too few to fill the chip with whole ones
-// and up to 64 columns four waves of 16.
+//          whole heads would leave CUs empty
+// and up to 64 columns four waves of 16.  Whole chains of 4096 tokens, H=16,
+// d=128, bf16, SPLIT and WIDE: 128 chains 193 and 262 us, 192 chains 369 and
+// 264, 512 chains 760 and 491.  Segments, WIDE and TALL: 65536 tokens on 16
+// heads 388 and 411 us; the gradients (WIDE would not fit their registers)
+// are TALL.
 enum Form { WIDE, TALL, SPLIT };
 
 template <class T, int DX, int MODE, int NP, int NS, int NU>
 hipError_t launch_width(const SweepArgs &a, Form form, bool vec, hipStream_t s) {
-    if (a.dz <= 64 && form != SPLIT) return launch_shape<T, DX, 4, 1, 1, MODE, NP, NS, NU>(a, vec, s);
+    if (a.dz <= 64) return launch_shape<T, DX, 4, 1, 1, MODE, NP, NS, NU>(a, vec, s);
     if constexpr (MODE == OUT) {
         if (form == SPLIT) return launch_shape<T, DX, 4, 1, 2, MODE, NP, NS, NU>(a, vec, s);
         if (form == WIDE) return launch_shape<T, DX, 4, 2, 1, MODE, NP, NS, NU>(a, vec, s);
@@ -1427,7 +1448,7 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
     a.p_scale = a.s_scale = l.scale;
     // whole chains also give the final state: their updates keep 24 bits
     if (cut) return launch_typed<OUT, 2, 1, 2>(l, a, WIDE, vec, s);
-    return launch_typed<OUT, 2, 1, 3>(l, a, l.N * l.H >= 256 || l.dv <= 64 ? WIDE : SPLIT, vec, s);
+    return launch_typed<OUT, 2, 1, 3>(l, a, l.N * l.H > 128 ? WIDE : SPLIT, vec, s);
 }
 
 hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
