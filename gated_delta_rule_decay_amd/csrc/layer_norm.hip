@@ -8,7 +8,9 @@
 // of a wave (several rows a wave), or by a whole workgroup for long rows.  The
 // variance is the mean square of x - mean, taken from the registers, so it
 // does not cancel where the mean is large.  All sums are fp32 (the weight's
-// across workgroups fp64).
+// across workgroups fp64).  Measured, bf16: forward 524288 x 128 rows 55 us
+// (4.9 TB/s, the rate of a large copy), backward 32768 x 2048 with dw and db
+// 89 us (4.5 TB/s).
 #include <initializer_list>
 #include <type_traits>
 
@@ -295,15 +297,23 @@ struct Plan {
     int rows;  // rows of a workgroup
 };
 
-// Lanes and registers of a row: as few lanes as hold it.  A wave keeps up to
-// 4 vectors (16 elements without them) a lane, a workgroup of 256 lanes 32
-// elements, one of 1024 lanes (half the registers a lane) 16.
-Plan plan_of(const NormArgs &a, bool vec) {
+// Vectors that a lane of a row within a wave holds at most.  Forward: with 2,
+// wider rows go to a workgroup each (32768 x 2048 bf16: 53 us, with 4 in a
+// wave 56; 64 rows: 4.2 and 5.4).  Backward: 4 (89 us, with 2 93).
+constexpr int FWD_WAVE = 2, BWD_WAVE = 4;
+
+// Lanes and registers of a row: as few lanes as hold it, since the sums over
+// a workgroup cost two barriers each and those of 1024 lanes most (16384 x
+// 4096 bf16 forward: 54 us with 256 lanes, 97 with 1024).  256 lanes hold up
+// to 32 elements each, backward 16 where they are vectors (8192 x 8192 bf16:
+// 138 us with 256 lanes of 32 elements, 118 with 1024 of 8; 16384 x 4096: 90
+// with 256 of 16, 158 with 1024), 1024 lanes (half the registers) 16.
+Plan plan_of(const NormArgs &a, bool vec, bool backward) {
     Plan p;
     p.ve = vec ? (a.bf16 ? 8 : 4) : 1;
     const int64_t n = (a.D + p.ve - 1) / p.ve;  // vectors of a row
-    const int most = vec ? 4 : 16;
-    p.block = n <= 64 * most ? 0 : a.D <= 256 * 32 ? 256 : 1024;
+    const int most = !vec ? 16 : backward ? BWD_WAVE : FWD_WAVE;
+    p.block = n <= 64 * most ? 0 : a.D <= 256 * (vec && backward ? 16 : 32) ? 256 : 1024;
     if (p.block) {
         p.threads = p.tpr = p.block;
         p.rows = 1;
@@ -333,8 +343,20 @@ int64_t grid_of(const NormArgs &a, const Plan &p, int64_t want) {
     const int64_t n = need < want ? need : want;
     return (n + unit - 1) / unit * unit;
 }
-int64_t fwd_grid(const NormArgs &a, const Plan &p) { return grid_of(a, p, p.threads == 1024 ? 512 : 2048); }
-int64_t bwd_grid(const NormArgs &a, const Plan &p) { return grid_of(a, p, p.threads == 1024 ? 256 : 1024); }
+int64_t fwd_grid(const NormArgs &a, const Plan &p) { return grid_of(a, p, p.threads == 1024 ? 256 : 2048); }
+// Backward: as many workgroups as run at once, for 256 CUs.  A second round
+// of a few more leaves most CUs idle, and every workgroup adds partial sums.
+// What runs at once follows from the registers that the elements of a lane
+// take: up to 8 elements four a CU (524288 x 128 bf16: 85 us, three 91), 16
+// three (65536 x 1024: 84, four 102; 16384 x 4096: 90, four 115), without
+// vectors two (65536 x 509 fp32: 103, three 128), 32 two in waves (32768 x
+// 2048: 89, three 103, four 96), one over a workgroup (4096 x 8191: 99, two
+// 115), and one of 1024 lanes (8192 x 8192: 118, two 121).
+int64_t bwd_grid(const NormArgs &a, const Plan &p) {
+    const int held = p.ve * p.nv;
+    const int per_cu = p.block == 1024 ? 1 : held <= 8 ? 4 : held <= 16 ? (p.ve > 1 ? 3 : 2) : p.block ? 1 : 2;
+    return grid_of(a, p, 256 * per_cu);
+}
 
 // rows of the partial sums
 int64_t slots_of(const NormArgs &a, const Plan &p) {
@@ -347,12 +369,12 @@ bool vector_ok(const NormArgs &a, std::initializer_list<const void *> ps) {
     return ok;
 }
 
-template <class T, class F>
+template <class T, int WAVE, class F>
 hipError_t dispatch(const Plan &p, F go) {
     using std::integral_constant;
     auto pick = [&](auto ve, auto block) -> hipError_t {
         constexpr int VE = decltype(ve)::value, B = decltype(block)::value;
-        constexpr int MOST = (B == 0 ? (VE > 1 ? 4 * VE : 16) : B == 256 ? 32 : 16) / VE;  // vectors of a lane
+        constexpr int MOST = (B == 0 ? (VE > 1 ? WAVE * VE : 16) : B == 256 ? (VE > 1 && WAVE == BWD_WAVE ? 16 : 32) : 16) / VE;  // vectors of a lane
         hipError_t e = hipErrorInvalidValue;
         auto use = [&](auto nv) {
             if constexpr (decltype(nv)::value <= MOST) e = go(ve, nv, block);
@@ -375,10 +397,10 @@ hipError_t dispatch(const Plan &p, F go) {
 
 template <class T>
 hipError_t fwd(const NormArgs &a, hipStream_t s) {
-    const Plan p = plan_of(a, vector_ok(a, {a.x, a.y, a.w, a.b}));
+    const Plan p = plan_of(a, vector_ok(a, {a.x, a.y, a.w, a.b}), false);
     const int64_t grid = fwd_grid(a, p);
     if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    return dispatch<T>(p, [&](auto ve, auto nv, auto block) {
+    return dispatch<T, FWD_WAVE>(p, [&](auto ve, auto nv, auto block) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, decltype(ve)::value, decltype(nv)::value, decltype(block)::value>),
                            dim3(static_cast<unsigned>(grid)), dim3(p.threads), 0, s, a, p.tpr);
         return hipGetLastError();
@@ -387,10 +409,10 @@ hipError_t fwd(const NormArgs &a, hipStream_t s) {
 
 template <class T>
 hipError_t bwd(const NormArgs &a, float *part, hipStream_t s) {
-    const Plan p = plan_of(a, vector_ok(a, {a.x, a.dy, a.dx, a.w}));
+    const Plan p = plan_of(a, vector_ok(a, {a.x, a.dy, a.dx, a.w}), true);
     const int64_t grid = bwd_grid(a, p), slots = slots_of(a, p);
     const size_t lds = !p.block && a.G == 1 ? 4 * a.D * sizeof(float) : 0;
-    hipError_t e = dispatch<T>(p, [&](auto ve, auto nv, auto block) {
+    hipError_t e = dispatch<T, BWD_WAVE>(p, [&](auto ve, auto nv, auto block) {
         hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(ve)::value, decltype(nv)::value, decltype(block)::value>),
                            dim3(static_cast<unsigned>(grid)), dim3(p.threads), lds, s, a, p.tpr, part);
         return hipGetLastError();
@@ -409,7 +431,7 @@ size_t norm_bwd_workspace(const NormArgs &a) {
     // the larger of the two ways a row may be held
     size_t most = 0;
     for (bool vec : {false, true}) {
-        const Plan p = plan_of(a, vec);
+        const Plan p = plan_of(a, vec, true);
         const size_t n = static_cast<size_t>(slots_of(a, p) * a.D) * 8;
         most = n > most ? n : most;
     }

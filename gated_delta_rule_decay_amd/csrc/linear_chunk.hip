@@ -997,8 +997,10 @@ struct DecayArgs {
     int H, nseg, L, la_tok, half;  // half: chunks of 32 tokens, not 64
 };
 
-__global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
-    __shared__ double red[16];
+template <int NTH>
+__global__ void __launch_bounds__(NTH) decay_grad_kernel(DecayArgs a) {
+    constexpr int NW = NTH / 64;
+    __shared__ double red[NW];
     const int64_t sh = blockIdx.x, seg = sh / a.H;
     const int h = static_cast<int>(sh - seg * a.H), tid = threadIdx.x, lane = tid & 63;
     if (a.pfx && seg >= a.pfx[a.N]) return;
@@ -1028,13 +1030,13 @@ __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
     const float *d = a.d_tab + sh * a.dkv;
     double x = 0.0;
     if (a.dkv % 4 == 0) {
-        for (int64_t e = 4 * tid; e < a.dkv; e += 4096) {
+        for (int64_t e = 4 * tid; e < a.dkv; e += 4 * NTH) {
             const float4 p = *reinterpret_cast<const float4 *>(s + e), q = *reinterpret_cast<const float4 *>(d + e);
             x += (static_cast<double>(p.x) * q.x + static_cast<double>(p.y) * q.y) +
                  (static_cast<double>(p.z) * q.z + static_cast<double>(p.w) * q.w);
         }
     } else {
-        for (int64_t e = tid; e < a.dkv; e += 1024) x += static_cast<double>(s[e]) * d[e];
+        for (int64_t e = tid; e < a.dkv; e += NTH) x += static_cast<double>(s[e]) * d[e];
     }
     auto total = [&](double v) {  // over the workgroup, the same on every lane
 #pragma unroll
@@ -1044,7 +1046,7 @@ __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
         __syncthreads();
         v = 0.0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) v += red[w];
+        for (int w = 0; w < NW; ++w) v += red[w];
         return v;
     };
     x = total(x);
@@ -1053,7 +1055,7 @@ __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
     double sum = 0.0;
     const float *uq = a.uq + static_cast<int64_t>(h) * a.tokens, *uk = a.uk + static_cast<int64_t>(h) * a.tokens;
     const float *um = a.m + static_cast<int64_t>(h) * a.tokens;
-    for (int64_t top = lo + (hi - lo + 63) / 64 * 64; top > lo; top -= 1024) {
+    for (int64_t top = lo + (hi - lo + 63) / 64 * 64; top > lo; top -= NTH) {
         const int64_t t = top - 1 - tid;
         const bool live = t >= lo && t < hi;
         const double upto = wave_prefix(live ? static_cast<double>(uq[t]) - static_cast<double>(uk[t]) : 0.0);
@@ -1067,7 +1069,7 @@ __global__ void __launch_bounds__(1024) decay_grad_kernel(DecayArgs a) {
         __syncthreads();
         double before = 0.0, all = 0.0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
+        for (int w = 0; w < NW; ++w) {
             before += w < (tid >> 6) ? red[w] : 0.0;
             all += red[w];
         }
@@ -1511,7 +1513,12 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
                    l.cu ? vp.seq : nullptr, l.cu ? vp.pfx : nullptr, l.N, l.T, base.tokens, c.segs, l.dk * l.dv, base.H,
                    base.nseg, c.L, l.la_tok, !l.bf16};
     if (c.segs * l.H > 0) {
-        hipLaunchKernelGGL(decay_grad_kernel, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(1024), 0, s, d);
+        // lanes for the segment's tokens: 576 segments of at most 512 tokens 16 us with 1024 lanes
+        // (the chip holds 512 such workgroups) and 8 with 256, 256 of 1024 tokens 14 and 20
+        if (c.L <= 512)
+            hipLaunchKernelGGL(decay_grad_kernel<256>, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(256), 0, s, d);
+        else
+            hipLaunchKernelGGL(decay_grad_kernel<1024>, dim3(static_cast<unsigned>(c.segs * l.H)), dim3(1024), 0, s, d);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!l.la_tok) {

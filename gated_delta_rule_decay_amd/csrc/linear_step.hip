@@ -3,22 +3,26 @@
 //
 // Bound by HBM: the state is read and written once (8 dk dv bytes against
 // 4 dk dv operations).  The columns of the state are independent of each
-// other, so a workgroup takes a slab of CW columns of one head: 128 where
-// there are heads enough to fill the chip, 32 where there are few and the
-// latency of one workgroup's loads counts.  All of a lane's loads are issued
-// before the first is used.
+// other, so a workgroup takes a slab of CW = 32 columns of one head: with few
+// heads the latency of one workgroup's loads counts (16 heads of 128 x 128:
+// 3.9 us, with slabs of 128 6.4), with many the slabs' loads and stores
+// overlap (4096 heads: 104 us, 5.2 TB/s, 128: 114; only states that the cache
+// holds gain from wide slabs, 1024 heads: 24.9 and 21.6).  All of a lane's
+// loads are issued before the first is used.
 #include "common.h"
 #include "linear.h"
 
 namespace gdn2 {
 namespace {
 
+constexpr int CW = 32;  // columns of a workgroup
+
 template <int V>
 struct Vec {
     float e[V];
 };
 
-template <int V, int CW>
+template <int V>
 __global__ void __launch_bounds__(256) linear_step_kernel(LinStepArgs a, int slabs) {
     constexpr int CL = CW / V, RG = 256 / CL, ROWS = (128 + RG - 1) / RG;  // lanes of a row, row groups
     __shared__ float s_k[128], s_q[128];
@@ -75,11 +79,11 @@ __global__ void __launch_bounds__(256) linear_step_kernel(LinStepArgs a, int sla
                   a.bf16);
 }
 
-template <int V, int CW>
+template <int V>
 hipError_t go(const LinStepArgs &a, hipStream_t s) {
     const int64_t slabs = (a.dv + CW - 1) / CW, grid = a.N * a.H * slabs;
     if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((linear_step_kernel<V, CW>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a,
+    hipLaunchKernelGGL((linear_step_kernel<V>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a,
                        static_cast<int>(slabs));
     return hipGetLastError();
 }
@@ -88,8 +92,7 @@ hipError_t go(const LinStepArgs &a, hipStream_t s) {
 
 hipError_t launch_linear_step(const LinStepArgs &a, hipStream_t s) {
     const bool vec = a.dv % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;
-    if (!vec) return go<1, 32>(a, s);
-    return a.N * a.H >= 1024 ? go<4, 128>(a, s) : go<4, 32>(a, s);
+    return vec ? go<4>(a, s) : go<1>(a, s);
 }
 
 }  // namespace gdn2
