@@ -229,6 +229,12 @@ def test_many_rounds(g, shape, heads, dtype):
     check_all(g, *make(shape, dtype, shape[-2:] if heads else shape[-1:], F32, seed=3))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape,heads", [((700, 8192), False), ((130, 5, 5000), True), ((4200, 1536), False), ((290, 8193), False)])
+def test_many_rounds_of_wide_rows(g, shape, heads, dtype):
+    check_all(g, *make(shape, dtype, shape[-2:] if heads else shape[-1:], F32, seed=shape[-1]))
+
+
 def test_bad_rows_stay_alone(g):
     x, w, b, dy = gpu(*make((40, 3, 72), BF, (3, 72), F32))
     one = g.layer_norm_fwd(x, w, b)

@@ -386,6 +386,21 @@ def test_forward_many_chains(g, B, H, dtype):
     ref.check("state", S, S_ref, ref.F32)
 
 
+# enough chains that a segment is longer than 512 tokens: the widest sums of
+# the decay's gradient, over one segment and a part of a second
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,decay", [(1100, "token"), (1024, "head"), (577, "resets")])
+def test_backward_many_chains(g, T, decay, dtype):
+    d = make(3, T, 171, 16, 24, dtype, decay=decay, seed=T)
+    want = ref.linear_backward(d["q"], d["k"], d["v"], d["la"], d["s0"], 0.7, d["d_o"], d["d_s"])
+    x = dev(d)
+    got = g.linear_chunk_bwd(x["q"], x["k"], x["v"], x["la"], x["s0"], x["d_o"], x["d_s"], q_scale=0.7)
+    torch.cuda.synchronize()
+    for n in want:
+        tol = ref.F32 if dtype == F32 or n in ("d_log_decay", "d_state0") else ref.TWO if n == "dv" else ref.ONE
+        ref.check(n, got[n], want[n], tol)
+
+
 def test_packed_many_heads(g):
     # whole sequences, one workgroup each: an empty one among them
     lens, H = [70, 0, 1, 300], 130
