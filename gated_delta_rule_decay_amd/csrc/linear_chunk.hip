@@ -467,6 +467,9 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 #pragma unroll
         for (int t = 0; t < NT; ++t) S[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const bool all_ch = a.dx == DX;
+    // fp32: blocks of 32 channels that the rows do not have are passed over
+    const int live_ch = __builtin_amdgcn_readfirstlane(a.dx);
+    auto past = [&](int ch) { return ESZ == 4 && ch >= live_ch; };
     int soff[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -591,9 +594,11 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
             auto product = [&](int it, int jt) {
                 f32x4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KS; ++ks) {
+                    if (past(32 * ks)) break;
                     sc = E::mma(TX::row_frag(s_y + 16 * jt * TX::BYTES, ls, 4 * ks + g),
                                 TX::row_frag(s_x + 16 * it * TX::BYTES, ls, 4 * ks + g), sc);
+                }
                 return sc;
             };
             auto pairs = [&](int it, int jt) {  // w_i . z_j
@@ -673,6 +678,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                 for (int t = 0; t < NT; ++t) O[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < KSW; ++ks) {
+                if (past(ch0 + 32 * ks)) break;
                 Frag sf[NT][NS];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -735,6 +741,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
             }
 #pragma unroll
             for (int m = 0; m < MT; m += 2) {  // two tiles at a time: independent products between dependent ones
+                if (past(ch0 + 16 * m)) break;
                 const int un = (ch0 >> 3) + 4 * (m >> 1) + (lane & 3);
                 const Frag y0 = TX::col_frag(s_y, kt, un, 0, lane), y1 = TX::col_frag(s_y, kt, un, 1, lane);
 #pragma unroll
