@@ -405,7 +405,13 @@ struct Shape {
 //
 // The operands made here are rounded to bf16 parts: the score matrix to NP of
 // them, the state to NS, the decayed values that update the state to NU (three
-// parts hold all 24 bits; fp32 inputs are not split).
+// parts hold all 24 bits; fp32 inputs are not split).  Where only bf16 results
+// follow, two parts: they leave 2^-16 of an operand, where the result's own
+// rounding leaves 2^-8.  Against fp64, o and dv are then as far off as fp32
+// sums rounded once (relative 1.66e-3; with the state in one part up to
+// 2.25e-3 where it dominates).  Three parts everywhere give the same 1.66e-3
+// and take 234 us for 207 (8 x 4096 tokens, H=16, d=128) and 555 for 409
+// (65536 tokens).
 //
 // OUTU and OUTM (all of z's columns in one workgroup): per token what it adds
 // to the decay's gradient, through the state and (OUTM) inside its chunk,
@@ -676,7 +682,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) O[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (NS > 1) {
+            if constexpr (MODE >= OUTU && NS > 1) {
                 // The small parts of all channels first: what a matrix
                 // instruction adds is cut to fp32 at the size that the sum has
                 // by then.  Here and in the state's update it takes the error
@@ -711,25 +717,28 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                                 for (int k = 0; k < 2; ++k) O[rt + k][t] = E::mma(sf[ks][t][q], xf[k][ks], O[rt + k][t]);
                 }
             } else {
+                // One block of channels at a time, its small part first: all
+                // channels' parts at once do not fit two workgroups' registers.
 #pragma unroll
-            for (int ks = 0; ks < KSW; ++ks) {
-                if (past(ch0 + 32 * ks)) break;
-                Frag sf[NT][1];
+                for (int ks = 0; ks < KSW; ++ks) {
+                    if (past(ch0 + 32 * ks)) break;
+                    Frag sf[NT][NS];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float v[8];
+                    for (int t = 0; t < NT; ++t) {
+                        float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = S[2 * ks + (e >> 2)][t][e & 3];
-                    E::template split<1>(v, sf[t]);
+                        for (int e = 0; e < 8; ++e) v[e] = S[2 * ks + (e >> 2)][t][e & 3];
+                        E::template split<NS>(v, sf[t]);
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const Frag xf = TX::row_frag(s_x + 16 * rt * TX::BYTES, ls, (ch0 >> 3) + 4 * ks + g);
+#pragma unroll
+                        for (int q = NS - 1; q >= 0; --q)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) O[rt][t] = E::mma(sf[t][q], xf, O[rt][t]);
+                    }
                 }
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const Frag xf = TX::row_frag(s_x + 16 * rt * TX::BYTES, ls, (ch0 >> 3) + 4 * ks + g);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                            O[rt][t] = E::mma(sf[t][0], xf, O[rt][t]);
-                }
-            }
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -964,7 +973,7 @@ __global__ void __launch_bounds__(64 * NCW, 2) gradient_kernel(Sweeps a) {
     switch (in / each) {
         case 0: sweep_body<T, DX, NCW, 1, 1, OUTM, B ? 2 : 1, B ? 3 : 1, B ? 3 : 1, VEC>(a.s[0], sh, smem); break;
         case 1: sweep_body<T, DX, NCW, 1, 1, OUTU, B ? 2 : 1, B ? 3 : 1, B ? 3 : 1, VEC>(a.s[1], sh, smem); break;
-        default: sweep_body<T, DX, NCW, 1, 1, OUT, B ? 2 : 1, 1, B ? 2 : 1, VEC>(a.s[2], sh, smem); break;
+        default: sweep_body<T, DX, NCW, 1, 1, OUT, B ? 2 : 1, B ? 2 : 1, B ? 2 : 1, VEC>(a.s[2], sh, smem); break;
     }
 }
 
@@ -1498,8 +1507,8 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
     }
     a.p_scale = a.s_scale = l.scale;
     // whole chains also give the final state: their updates keep 24 bits
-    if (cut) return launch_typed<OUT, 2, 1, 2>(l, a, WIDE, vec, s);
-    return launch_typed<OUT, 2, 1, 3>(l, a, l.N * l.H > 128 ? WIDE : SPLIT, vec, s);
+    if (cut) return launch_typed<OUT, 2, 2, 2>(l, a, WIDE, vec, s);
+    return launch_typed<OUT, 2, 2, 3>(l, a, l.N * l.H > 128 ? WIDE : SPLIT, vec, s);
 }
 
 hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
@@ -1555,7 +1564,7 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     } else {
         if ((e = launch_typed<OUTM, 2, 3, 3>(l, q, TALL, vec, s)) != hipSuccess) return e;
         if ((e = launch_typed<OUTU, 2, 3, 3>(l, k, TALL, vec, s)) != hipSuccess) return e;
-        if ((e = launch_typed<OUT, 2, 1, 2>(l, v, TALL, vec, s)) != hipSuccess) return e;
+        if ((e = launch_typed<OUT, 2, 2, 2>(l, v, TALL, vec, s)) != hipSuccess) return e;
     }
 
     DecayArgs d = {f.uq, f.uk, f.um, f.s_tab, f.d_tab, f.s_fin, l.la, l.d_la, f.part, l.cu ? vp.tab : nullptr,

@@ -384,11 +384,11 @@ gdn2_status gdn2_recurrent_step(const gdn2_desc *desc,
  *
  * Precision, bf16 inputs: the products of inputs are exact, every sum is
  * fp32.  The masked scores enter their product as two bf16 parts (16 bits),
- * the state enters the read of o and dv as one bf16 (8 bits: about one more
- * rounding of the output's size) and of dq and dk as three, and the values
- * that update a state as three (all 24 bits), or two where only bf16 results
- * come of it; states, d_log_decay and d_state0 carry fp32 accuracy.
- * fp32 inputs: fp32 throughout.
+ * the state enters the read of o and dv as two and of dq and dk as three, and
+ * the values that update a state as three (all 24 bits), or two where only
+ * bf16 results come of it: two parts leave 2^-16 of an operand, a small share
+ * of the 2^-8 that the result's own rounding leaves.  States, d_log_decay and
+ * d_state0 carry fp32 accuracy.  fp32 inputs: fp32 throughout.
  *
  * Preconditions not checked: all values finite, log_decay <= 0 (minus
  * infinity is allowed and clears the state; anything below -10000 counts as
