@@ -37,6 +37,7 @@
 // state that enters each, and the sweeps then run over all segments at once.
 #include <initializer_list>
 
+#include "chunk_walk.h"
 #include "kernels.h"
 #include "linear.h"
 
@@ -534,7 +535,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
         sz.load(p0, len);
         if (MODE >= OUTU) sw.load(p0, len);
         if (wave == NW - 1)  // the decay of each position
-            la_next = load4(buffer(la_base + p0 * la_row), inside(p0 + lane + la_skip, len + la_skip) && lane < CT ? la_off : NOWHERE, 0);
+            la_next = load4(buffer(la_base + p0 * la_row), lane < CT && inside(p0 + lane + la_skip, len + la_skip) ? la_off : NOWHERE, 0);
     };
     // the loaded chunk into LDS, its decays summed
     auto stage_chunk = [&] {
@@ -572,9 +573,9 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
     }
     __syncthreads();
 
-    for (int p0 = begin; p0 < len; p0 += CT) {
+    for (int p0 = begin; len > 0; p0 += CT) {
         // the next chunk's loads, in two parts: a CU takes 64 bytes a cycle
-        const bool more = p0 + CT < len;
+        const bool more = chunk_follows(p0, len, CT);
         if (more) load_first(p0 + CT);
         if (MODE == STATE && more) load_second(p0 + CT);
 
@@ -905,6 +906,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                 }
             }
         }
+        if (!more) break;
         __syncthreads();  // the next chunk is staged, the scores read
     }
 
