@@ -991,22 +991,24 @@ struct ScanArgs {
     const float *la;
     int64_t N, T;
     int64_t dkv;
-    int H, nseg, rev, la_tok, blocks;  // blocks: workgroups of a state
+    int H, nseg, rev, la_tok;
 };
 
 struct Scans {
     ScanArgs s[2];
 };
 
-// V elements of the state a lane (V = 4: whole 16-byte units).
+// V elements of the state a lane (V = 4: whole 16-byte units).  One state a
+// workgroup of x, its blocks along y: up to 64 of them for 127 x 127 elements,
+// which together with 2^20 states would be more lanes than one axis may have.
 template <int V>
 __global__ void __launch_bounds__(256) segment_scan_kernel(Scans two) {
     constexpr int AHEAD = 8;  // segments whose loads are in flight together
     typedef float Fv __attribute__((ext_vector_type(V)));
-    const ScanArgs &a = two.s[blockIdx.y];
-    const int64_t sh = blockIdx.x / a.blocks, n = sh / a.H;
+    const ScanArgs &a = two.s[blockIdx.z];
+    const int64_t sh = blockIdx.x, n = sh / a.H;
     const int h = static_cast<int>(sh - n * a.H);
-    const int64_t e = (static_cast<int64_t>(blockIdx.x % a.blocks) * 256 + threadIdx.x) * V;
+    const int64_t e = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * V;
     if (e >= a.dkv) return;
     const int64_t s0 = a.pfx ? a.pfx[n] : n * a.nseg;
     const int cnt = a.pfx ? a.pfx[n + 1] - a.pfx[n] : a.nseg;
@@ -1356,16 +1358,16 @@ int granularity(const LinArgs &l, int64_t d, std::initializer_list<const void *>
     return g;
 }
 
-hipError_t launch_scans(Scans a, int n, hipStream_t s) {
+hipError_t launch_scans(const Scans &a, int n, hipStream_t s) {
     const int v = a.s[0].dkv % 4 == 0 ? 4 : 1;
-    for (int i = 0; i < n; ++i) a.s[i].blocks = static_cast<int>((a.s[i].dkv + 256 * v - 1) / (256 * v));
-    const int64_t grid = a.s[0].N * a.s[0].H * a.s[0].blocks;
-    if (grid <= 0) return hipSuccess;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
+    const int64_t states = a.s[0].N * a.s[0].H;
+    if (states <= 0) return hipSuccess;
+    if (states > 0x7fffffffLL) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(states), static_cast<unsigned>((a.s[0].dkv + 256 * v - 1) / (256 * v)), n);
     if (v == 4)
-        hipLaunchKernelGGL(segment_scan_kernel<4>, dim3(static_cast<unsigned>(grid), n), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(segment_scan_kernel<4>, grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL(segment_scan_kernel<1>, dim3(static_cast<unsigned>(grid), n), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(segment_scan_kernel<1>, grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1468,7 +1470,7 @@ BwdSpace bwd_space(const LinArgs &a, const Cut &c, void *ws) {
 bool linear_fits(const LinArgs &a, bool backward) {
     const Cut c = backward ? bwd_cut(a) : fwd_cut(a);
     // workgroups of up to 1024 lanes a segment and head, three of 512 in the
-    // gradient sweeps; 16 of 256 a state
+    // gradient sweeps; 256 a state along the scan's first axis
     const int64_t most = INT64_C(1) << 32, sh = c.segs * a.H + SWEEP_GROUP;
     return sh < most / (backward ? 1536 : 1024) && a.N * a.H < most / 4096;
 }
@@ -1502,7 +1504,7 @@ hipError_t launch_linear_fwd(const LinArgs &l, void *ws, hipStream_t s) {
         st.tot = f.tot;
         if ((e = launch_typed<STATE, 1, 1, 3>(l, st, TALL, vec, s)) != hipSuccess) return e;
         const ScanArgs sc = {f.tab, f.tot, l.s0, l.s_out, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
-                       l.dk * l.dv, a.H, a.nseg, 0, l.la_tok, 0};
+                       l.dk * l.dv, a.H, a.nseg, 0, l.la_tok};
         if ((e = launch_scans({{sc, {}}}, 1, s)) != hipSuccess) return e;
         a.s_in = f.tab;
         a.s_out = nullptr;
@@ -1540,7 +1542,7 @@ hipError_t launch_linear_bwd(const LinArgs &l, void *ws, hipStream_t s) {
     }
     Scans sc;
     sc.s[0] = {f.s_tab, f.s_tot, l.s0, f.s_fin, l.cu ? vp.pfx : nullptr, l.cu ? vp.seq : nullptr, l.la, l.N, l.T,
-               l.dk * l.dv, base.H, base.nseg, 0, l.la_tok, 0};
+               l.dk * l.dv, base.H, base.nseg, 0, l.la_tok};
     sc.s[1] = sc.s[0];
     sc.s[1].tab = f.d_tab; sc.s[1].tot = f.d_tot; sc.s[1].init = l.d_sT; sc.s[1].fin = l.d_s0; sc.s[1].rev = 1;
     if ((e = launch_scans(sc, 2, s)) != hipSuccess) return e;
