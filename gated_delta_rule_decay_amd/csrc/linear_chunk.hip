@@ -910,10 +910,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
         __syncthreads();  // the next chunk is staged, the scores read
     }
 
-    if (a.s_out) {
-        // in reverse order the state has yet to pass the first token's decay
-        float fin = 1.f;
-        if (MODE != STATE && rev && len > 0) fin = __expf(a.la[a.la_tok ? sg.lo * a.H + h : h]);
+    if (a.s_out) {  // (in reverse: the first token's decay is the scan's to apply)
         const auto b = buffer(a.s_out + sh * dkv, 4 * dkv);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -922,7 +919,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int ch = 32 * (m >> 1) + 4 * (m & 1) + r;
-                    store4(fin * S[m][t][r], b, all_ch || ch0 + ch + 8 * g < a.dx ? soff[t] : NOWHERE, 4 * ch * a.dz);
+                    store4(S[m][t][r], b, all_ch || ch0 + ch + 8 * g < a.dx ? soff[t] : NOWHERE, 4 * ch * a.dz);
                 }
     }
     if (MODE == STATE && a.tot && cb == 0 && tid == NTH - 64) a.tot[sh] = total;
