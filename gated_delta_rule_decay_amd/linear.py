@@ -342,18 +342,18 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     return out, mean, rstd
 
 
-def layer_norm_bwd(dy, x, weight, mean, rstd, want_weight=None, want_bias=False, workspace=None):
+def layer_norm_bwd(dy, x, weight, mean, rstd, want_weight=None, want_bias=False, workspace=None, bias=None):
     """Gradients of <dy, y> for ``layer_norm_fwd``: (dx, d_weight, d_bias).
 
     ``weight`` None: ones.  d_weight (``want_weight``: by default where weight
     is given) and d_bias (``want_bias``) have the weight's shape and type
-    ([D] fp32 without one), None where not wanted.  ``workspace``: None
-    allocates it, or a uint8 device tensor of at least
-    layer_norm_bwd_workspace() bytes.
+    (without one those of ``bias``, the forward's, which is not read; [D] fp32
+    without either), None where not wanted.  ``workspace``: None allocates it,
+    or a uint8 device tensor of at least layer_norm_bwd_workspace() bytes.
     """
     import torch
-    sizes = _norm_sizes(x, weight, None, 0.0)
-    dev, stat = x.device, x.shape[:-1]
+    sizes = _norm_sizes(x, weight, bias, 0.0)
+    dev, stat, first = x.device, x.shape[:-1], weight if weight is not None else bias
     _like(dy, "dy", x.shape, x.dtype, dev)
     _like(mean, "mean", stat, torch.float32, dev)
     _like(rstd, "rstd", stat, torch.float32, dev)
@@ -361,7 +361,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, want_weight=None, want_bias=False,
         want_weight = weight is not None
 
     def like():
-        return torch.empty(x.shape[-1:], dtype=torch.float32, device=dev) if weight is None else torch.empty_like(weight)
+        return torch.empty(x.shape[-1:], dtype=torch.float32, device=dev) if first is None else torch.empty_like(first)
 
     dx = torch.empty_like(x)
     dw, db = like() if want_weight else None, like() if want_bias else None
