@@ -27,10 +27,10 @@
 //
 // Bound by HBM (the forward reads q, k, v and writes o: 4 dk dv operations
 // for 2 (2 dk + 2 dv) bytes a token and head, a quarter of what a large
-// product reaches).  Measured, H=16, d=128, bf16, decays and an initial state:
-// 8 x 4096 tokens 193-203 us (2.9 TB/s; a large copy takes 113), 65536 tokens
-// 380 us (k and v read twice: 4.2 TB/s), the backward of 4 x 4096 tokens
-// 390-400 us.
+// product reaches).  Measured, H=16, d=128, bf16, decays and an initial state,
+// whole calls in a warm loop: 8 x 4096 tokens 200-212 us (2.7 TB/s; a large
+// copy takes 113), 65536 tokens 395-409 us (k and v read twice: 4.0 TB/s), the
+// backward of 4 x 4096 tokens 370-400 us.
 //
 // Long sequences are cut into segments: a state-only sweep forms what every
 // segment adds to the state, a scan over the segments turns these into the
@@ -689,7 +689,7 @@ __device__ __forceinline__ void sweep_body(const SweepArgs &a, int64_t item, cha
                 // by then.  Here and in the state's update it takes the error
                 // of d_log_decay from 9.1e-7 to 6.5e-7 (4 x 4096 tokens, H=16,
                 // d=128), and the products of two row tiles in turn take the
-                // gradient sweeps from 321 to 301 us (the shortest of 8 runs).
+                // whole backward from 377 to 372 us.
                 Frag sf[KSW][NT][NS];
 #pragma unroll
                 for (int ks = 0; ks < KSW; ++ks)
@@ -946,9 +946,9 @@ __global__ void __launch_bounds__(64 * NCW * KSP, 2) sweep_kernel(SweepArgs a) {
 // The two state sweeps of the backward, and its three gradient sweeps, in one
 // launch each.  The gradient sweeps go by groups of segments and heads, one
 // sweep after the other: most CUs then run the same instructions, and the
-// rows come from the caches the second and third time.  (All of one sweep
-// first: 5 % slower at 256 segments and heads of 1024 tokens; the three of a
-// segment next to each other: 20 % slower.)
+// rows come from the caches the second and third time.  (At 256
+// segments and heads of 1024 tokens the whole backward takes 372 us; all of one
+// sweep first 374, the three of a segment next to each other 398.)
 constexpr int SWEEP_GROUP = 128;
 
 struct Sweeps {
@@ -1246,8 +1246,9 @@ int64_t segment_tokens(const LinArgs &a, int64_t most) {
 
 // Forward: segments where whole chains leave the chip empty, two for each CU.
 // Measured (H=16, d=128, bf16), whole chains and segments: 64 chains of 4096
-// tokens 185 and 114 us, 128 chains 193 and 214; 16 chains of 512 tokens 28
-// and 30 us, of 1024 49 and 34 (fp32, 256 tokens: 38 and 45; 512: 68 and 49).
+// tokens 194 and 130 us, 112 chains 197 and 206, 128 chains 206 and 230, 192
+// chains 274 and 356; 16 chains of 512 tokens 29 and 27 us, of 1024 53 and 30
+// (fp32, 256 tokens: 39 and 41; 512: 73 and 43).
 Cut fwd_cut(const LinArgs &a) {
     const int64_t heads = a.H * (a.cu ? 1 : a.N);
     if (a.T <= (a.bf16 ? 512 : 256) || heads >= 112) return Cut{0, 1, a.N};
@@ -1259,8 +1260,9 @@ Cut fwd_cut(const LinArgs &a) {
 
 // Backward: always through the segments' states, at most 1024 tokens apart,
 // which bounds how far the differences of the decay's gradient are summed.
-// One gradient sweep of eight waves fills a CU (2048 or 512 tokens at 64
-// chains: 7 and 12 % slower), or two of four waves.
+// One gradient sweep of eight waves fills a CU (64 chains of 4096 tokens, the
+// whole call: 372 us, with segments of 2048 or 512 tokens 406 and 412), or two
+// of four waves.
 Cut bwd_cut(const LinArgs &a) {
     const int64_t L = segment_tokens(a, a.dk > 64 || a.dv > 64 ? 256 : 512);
     return cut_of(a, L < 64 ? 64 : L > 1024 ? 1024 : L);
@@ -1295,11 +1297,19 @@ hipError_t launch_shape(SweepArgs a, bool vec, hipStream_t s) {
 //   SPLIT  64 columns, four pairs of waves, each pair sharing 16 columns and
 //          taking half of the channels: eight waves on half of a head, where
 //          whole heads would leave CUs empty
-// and up to 64 columns four waves of 16.  Whole chains of 4096 tokens, H=16,
-// d=128, bf16, SPLIT and WIDE: 128 chains 193 and 262 us, 192 chains 369 and
-// 264, 512 chains 760 and 491.  Segments, WIDE and TALL: 65536 tokens on 16
-// heads 388 and 411 us; the gradients (WIDE would not fit their registers)
-// are TALL.
+// and up to 64 columns four waves of 16.  Whole chains, SPLIT, TALL and WIDE:
+//   bf16, 4096 tokens, 128 x 128   128 chains 204 271 468 us, 144 385 272 472,
+//                                  256 407 312 503, 512 815 615 720
+//   bf16, 4096 tokens,  64 x 128   128 chains 163 204 204, 256 275 235 218,
+//                                  512 545 465 383
+//   fp32, 1024 tokens, 128 x 128   128 chains 145 209 212, 256 254 219 216,
+//                                  512 500 431 377
+// In bf16 above 64 channels WIDE's update in three parts takes more than its
+// 256 registers (35 spilled, and their loads wait behind the next chunk's
+// rows), so TALL stands in for it.  Segments (an update in two parts, 8
+// spilled), WIDE and TALL: 65536 tokens on 16 heads 402 and 430 us, fp32 7777
+// packed tokens on 5 heads 79 and 87.  The gradients (WIDE would not fit their
+// registers) are TALL.
 enum Form { WIDE, TALL, SPLIT };
 
 template <class T, int DX, int MODE, int NP, int NS, int NU>
@@ -1307,7 +1317,8 @@ hipError_t launch_width(const SweepArgs &a, Form form, bool vec, hipStream_t s) 
     if (a.dz <= 64) return launch_shape<T, DX, 4, 1, 1, MODE, NP, NS, NU>(a, vec, s);
     if constexpr (MODE == OUT) {
         if (form == SPLIT) return launch_shape<T, DX, 4, 1, 2, MODE, NP, NS, NU>(a, vec, s);
-        if (form == WIDE) return launch_shape<T, DX, 4, 2, 1, MODE, NP, NS, NU>(a, vec, s);
+        if constexpr (sizeof(T) == 4 || DX == 64 || NU < 3)
+            if (form == WIDE) return launch_shape<T, DX, 4, 2, 1, MODE, NP, NS, NU>(a, vec, s);
     }
     return launch_shape<T, DX, 8, 1, 1, MODE, NP, NS, NU>(a, vec, s);
 }

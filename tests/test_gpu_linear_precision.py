@@ -54,7 +54,7 @@ def hold_dv(dv, s, scale):
 # whole chains: half heads, one wave a column tile up to 64 columns, whole
 # heads above 128 chains; the second line in segments, on both sides of 64
 @pytest.mark.parametrize("decay", ["token", "head"])
-@pytest.mark.parametrize("B,T,H,dk,dv", [(2, 201, 3, 128, 128), (1, 64, 4, 100, 127), (2, 130, 3, 72, 56), (3, 90, 43, 64, 80),
+@pytest.mark.parametrize("B,T,H,dk,dv", [(2, 201, 3, 128, 128), (1, 64, 4, 100, 127), (2, 130, 3, 72, 56), (3, 90, 43, 64, 80), (3, 90, 43, 72, 80),
                                          (1, 700, 3, 128, 128), (1, 1100, 2, 66, 75), (2, 700, 3, 128, 64)])
 def test_forward(g, B, T, H, dk, dv, decay):
     s = make(B, T, H, dk, dv, BF, decay=decay, seed=T + dv)
