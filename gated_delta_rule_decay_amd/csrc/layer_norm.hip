@@ -8,9 +8,10 @@
 // of a wave (several rows a wave), or by a whole workgroup for long rows.  The
 // variance is the mean square of x - mean, taken from the registers, so it
 // does not cancel where the mean is large.  All sums are fp32 (the weight's
-// across workgroups fp64).  Measured, bf16: forward 524288 x 128 rows 55 us
-// (4.9 TB/s, the rate of a large copy), backward 32768 x 2048 with dw and db
-// 89 us (4.5 TB/s).
+// across workgroups fp64).  Measured, bf16, whole calls in a warm loop: forward
+// 524288 x 128 rows 56 us (4.8 TB/s, the rate of a large copy), backward 32768
+// x 2048 with dw and db 86 us (4.7 TB/s).  The figures at the launch rules
+// below are of replayed graphs on two inputs in turn.
 #include <initializer_list>
 #include <type_traits>
 

@@ -218,8 +218,8 @@ def linear_chunk_fwd(q, k, v, log_decay, state0=None, q_scale=1.0, out=None, sta
 
     q, k [B,T,H,dk], v [B,T,H,dv] (bf16 or fp32, one dtype); log_decay fp32
     [B,T,H], or [H] for one value per head; state0 [B,H,dk,dv] fp32 or None.
-    ``workspace``: True allocates the scratch that long sequences on few
-    chains run in parallel segments with, False runs without, or a uint8
+    ``workspace``: True (or None) allocates the scratch that long sequences on
+    few chains run in parallel segments with, False runs without, or a uint8
     device tensor of at least linear_chunk_fwd_workspace() bytes.
     Returns (o like v, final state [B,H,dk,dv] fp32 or None).
     """
@@ -232,6 +232,8 @@ def linear_chunk_fwd_varlen(q, k, v, log_decay, cu_seqlens, state0=None, q_scale
 
     q, k [T,H,dk], v [T,H,dv], log_decay [T,H] or [H] (or all but [H] with a
     leading 1); cu_seqlens int32 [N+1] on the device; states [N,H,dk,dv].
+    Tokens outside every sequence are not written: a given ``out`` keeps
+    them, a new one has any value there.
     """
     return _fwd(q, k, v, log_decay, cu_seqlens, state0, q_scale, out, state_out, return_state, workspace)
 
@@ -277,7 +279,10 @@ def linear_chunk_bwd(q, k, v, log_decay, state0, d_o, d_state=None, q_scale=1.0,
 
 def linear_chunk_bwd_varlen(q, k, v, log_decay, cu_seqlens, state0, d_o, d_state=None, q_scale=1.0, want_state0=None,
                             workspace=None):
-    """``linear_chunk_bwd`` for ``linear_chunk_fwd_varlen``: packed tensors, states [N,H,dk,dv]."""
+    """``linear_chunk_bwd`` for ``linear_chunk_fwd_varlen``: packed tensors, states [N,H,dk,dv].
+
+    Gradients of tokens outside every sequence are not written (any value).
+    """
     return _bwd(q, k, v, log_decay, cu_seqlens, state0, d_o, d_state, q_scale, want_state0, workspace)
 
 

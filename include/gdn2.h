@@ -390,9 +390,18 @@ gdn2_status gdn2_recurrent_step(const gdn2_desc *desc,
  * of the 2^-8 that the result's own rounding leaves.  States, d_log_decay and
  * d_state0 carry fp32 accuracy.  fp32 inputs: fp32 throughout.
  *
+ * d_log_decay is a sum over the tokens behind, so its rounding errors are of
+ * the size of what is summed, also where a token's own gradient is next to
+ * nothing (a far decay's) or a head's terms cancel.
+ *
  * Preconditions not checked: all values finite, log_decay <= 0 (minus
  * infinity is allowed and clears the state; anything below -10000 counts as
  * -10000, whose exponential is 0).
+ *
+ * GDN2_ERR_UNSUPPORTED: dk or dv above 128, a sequence of 2^31 tokens or
+ * more, more than 65535 heads, 2^20 (sequence, head) states or more, and
+ * requests of more than 2.7 million (segment, head) pairs backward or 4.1
+ * million forward (a segment: at most 1024 tokens backward).
  */
 typedef enum gdn2_decay_kind {
     GDN2_DECAY_TOKEN = 0, /* log_decay [B,T,H]: one value per token and head */
