@@ -28,7 +28,11 @@ EXPORTS = ("gdn2_abi_version", "gdn2_status_str", "gdn2_chunk_fwd_workspace",
            "gdn2_chunk_bwd_varlen", "gdn2_recurrent_step",
            "gdn2_linear_fwd_workspace", "gdn2_linear_fwd", "gdn2_linear_fwd_varlen_workspace", "gdn2_linear_fwd_varlen",
            "gdn2_linear_bwd_workspace", "gdn2_linear_bwd", "gdn2_linear_bwd_varlen_workspace", "gdn2_linear_bwd_varlen",
-           "gdn2_linear_step", "gdn2_layer_norm_fwd", "gdn2_layer_norm_bwd_workspace", "gdn2_layer_norm_bwd")
+           "gdn2_linear_step", "gdn2_layer_norm_fwd", "gdn2_layer_norm_bwd_workspace", "gdn2_layer_norm_bwd",
+           "gdn2_rotary_fwd", "gdn2_rotary_bwd", "gdn2_qk_norm_fwd", "gdn2_qk_norm_bwd_workspace", "gdn2_qk_norm_bwd",
+           "gdn2_scan_fwd_workspace", "gdn2_scan_fwd", "gdn2_scan_fwd_varlen_workspace", "gdn2_scan_fwd_varlen",
+           "gdn2_scan_bwd_workspace", "gdn2_scan_bwd", "gdn2_scan_bwd_varlen_workspace", "gdn2_scan_bwd_varlen",
+           "gdn2_scan_step")
 
 
 class Gdn2Desc(ctypes.Structure):

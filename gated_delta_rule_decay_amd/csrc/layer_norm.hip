@@ -16,22 +16,11 @@
 #include <type_traits>
 
 #include "common.h"
+#include "elements.h"
 #include "linear.h"
 
 namespace gdn2 {
 namespace {
-
-template <class T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32<uint16_t>(uint16_t x) { return bf16_to_f32(x); }
-
-template <class T, int VE>
-struct alignas(VE * sizeof(T) < 16 ? VE * sizeof(T) : 16) Pack {
-    T e[VE];
-};
 
 // VE elements at p + c; columns past D read as zero (VE > 1: D is a multiple).
 template <class T, int VE>

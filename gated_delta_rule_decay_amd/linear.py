@@ -31,25 +31,19 @@ class Gdn2NormDesc(ctypes.Structure):
     ]
 
 
+_signatures = []  # (entry point, argument types)
 _calls = {}  # entry point -> ctypes function
+
+
+def _register(*signatures):
+    _signatures.extend(signatures)
 
 
 def _lib():
     lib = load_library()
-    if not _calls:
-        vp, sz = ctypes.c_void_p, ctypes.c_size_t
-        ld, nd, szp = ctypes.POINTER(Gdn2LinearDesc), ctypes.POINTER(Gdn2NormDesc), ctypes.POINTER(ctypes.c_size_t)
+    if len(_calls) != len(_signatures):
         ready = {}
-        for name, args in (
-                ("gdn2_linear_fwd_workspace", [ld, szp]), ("gdn2_linear_fwd", [ld] + [vp] * 8 + [sz, vp]),
-                ("gdn2_linear_fwd_varlen_workspace", [ld, szp]),
-                ("gdn2_linear_fwd_varlen", [ld] + [vp] * 9 + [sz, vp]),
-                ("gdn2_linear_bwd_workspace", [ld, szp]), ("gdn2_linear_bwd", [ld] + [vp] * 13 + [sz, vp]),
-                ("gdn2_linear_bwd_varlen_workspace", [ld, szp]),
-                ("gdn2_linear_bwd_varlen", [ld] + [vp] * 14 + [sz, vp]),
-                ("gdn2_linear_step", [ld] + [vp] * 7),
-                ("gdn2_layer_norm_fwd", [nd] + [vp] * 7), ("gdn2_layer_norm_bwd_workspace", [nd, szp]),
-                ("gdn2_layer_norm_bwd", [nd] + [vp] * 9 + [sz, vp])):
+        for name, args in _signatures:
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = ctypes.c_int, args
             ready[name] = fn
@@ -57,8 +51,19 @@ def _lib():
     return lib
 
 
+_vp, _sz, _szp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+_ld, _nd = ctypes.POINTER(Gdn2LinearDesc), ctypes.POINTER(Gdn2NormDesc)
+_register(("gdn2_linear_fwd_workspace", [_ld, _szp]), ("gdn2_linear_fwd", [_ld] + [_vp] * 8 + [_sz, _vp]),
+          ("gdn2_linear_fwd_varlen_workspace", [_ld, _szp]), ("gdn2_linear_fwd_varlen", [_ld] + [_vp] * 9 + [_sz, _vp]),
+          ("gdn2_linear_bwd_workspace", [_ld, _szp]), ("gdn2_linear_bwd", [_ld] + [_vp] * 13 + [_sz, _vp]),
+          ("gdn2_linear_bwd_varlen_workspace", [_ld, _szp]), ("gdn2_linear_bwd_varlen", [_ld] + [_vp] * 14 + [_sz, _vp]),
+          ("gdn2_linear_step", [_ld] + [_vp] * 7),
+          ("gdn2_layer_norm_fwd", [_nd] + [_vp] * 7), ("gdn2_layer_norm_bwd_workspace", [_nd, _szp]),
+          ("gdn2_layer_norm_bwd", [_nd] + [_vp] * 9 + [_sz, _vp]))
+
+
 def _call(name):
-    if not _calls:
+    if name not in _calls:
         _lib()
     return _calls[name]
 

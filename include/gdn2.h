@@ -538,6 +538,185 @@ gdn2_status gdn2_layer_norm_bwd(const gdn2_norm_desc *desc, const void *dy, cons
                                 const float *mean, const float *rstd, void *dx, void *d_weight, void *d_bias,
                                 void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions and norms of queries and keys: what stands in front of a
+ * mixer.  Every head's first `rotary` channels hold pairs (u, v), which turn
+ * by the token's position times the pair's frequency,
+ *
+ *     u' = m (cos(t) u - sin(t) v),   v' = m (sin(t) u + cos(t) v),
+ *     t  = position * freq[j],        m  = magnitude
+ *
+ * for j = 0 .. rotary/2 - 1; the other channels pass.  The norms divide each
+ * token's q and k of each head by r and multiply by a weight first:
+ *
+ *     GDN2_QK_RMS: r = sqrt(mean x^2 + eps),   GDN2_QK_L2: r = sqrt(sum x^2)
+ *
+ * over the `dim` channels (eps takes no part in GDN2_QK_L2); a row of zeros
+ * stays zero, with a zero gradient where r is 0.
+ *
+ * q [tokens, q_heads, dim] and k [tokens, k_heads, dim] (k_heads may be 0)
+ * are read with q_stride and k_stride elements between tokens, so that they
+ * may be slices of one fused projection; everything written is contiguous.
+ * Gradients read by gdn2_rotary_bwd take the strides too, those read by
+ * gdn2_qk_norm_bwd are contiguous.  Token r stands at position
+ *     offset + positions[r % period]     (positions: device int32 [period])
+ *     offset + r % period                (positions NULL)
+ * so period = tokens gives every token its own and period = T with tokens =
+ * B * T shares them among the batch.  freq: device fp64 [rotary/2], radians a
+ * position; angles are formed in 64 bits, so far positions lose nothing.
+ * Arithmetic is fp32 (the norms' sums of squares and 1/r fp64: values of any
+ * size), results are rounded once.
+ */
+typedef enum gdn2_rotary_layout {
+    GDN2_ROTARY_HALF = 0,       /* pairs (x[j], x[j + rotary/2]) */
+    GDN2_ROTARY_INTERLEAVED = 1 /* pairs (x[2j], x[2j + 1])      */
+} gdn2_rotary_layout;
+
+typedef enum gdn2_qk_norm { GDN2_QK_NONE = 0, GDN2_QK_RMS = 1, GDN2_QK_L2 = 2 } gdn2_qk_norm;
+
+typedef struct gdn2_rotary_desc {
+    int64_t tokens;       /* 0 .. 2^31 - 1, a multiple of period */
+    int64_t period;       /* >= 1 */
+    int64_t q_heads;      /* >= 1, up to 65535 */
+    int64_t k_heads;      /* >= 0, up to 65535; 0: no k */
+    int64_t dim;          /* channels of a head, 1..256 */
+    int64_t rotary;       /* channels that turn: even, 0..dim (0: norm alone) */
+    int64_t q_stride;     /* elements from token to token, >= q_heads * dim */
+    int64_t k_stride;     /* the same of k, >= k_heads * dim */
+    int64_t offset;       /* added to every position, within +-2^40 */
+    int32_t dtype;        /* gdn2_dtype of q, k, the outputs and their gradients */
+    int32_t weight_dtype; /* gdn2_dtype of the weights and their gradients */
+    int32_t layout;       /* gdn2_rotary_layout */
+    int32_t norm;         /* gdn2_qk_norm: NONE for gdn2_rotary_*, else RMS or L2 */
+    float eps;            /* of GDN2_QK_RMS, >= 0 */
+    float magnitude;      /* finite */
+} gdn2_rotary_desc;
+
+/* The rotation alone.  q_out may be exactly q where q is contiguous
+ * (q_stride = q_heads * dim), and k_out k; outputs overlap nothing else. */
+gdn2_status gdn2_rotary_fwd(const gdn2_rotary_desc *desc, const void *q, const void *k, const double *freq,
+                            const int32_t *positions, void *q_out, void *k_out, void *stream);
+
+/* Its gradients: d_q_out, d_k_out (with the strides) turned back into dq, dk;
+ * in place as above. */
+gdn2_status gdn2_rotary_bwd(const gdn2_rotary_desc *desc, const void *d_q_out, const void *d_k_out, const double *freq,
+                            const int32_t *positions, void *dq, void *dk, void *stream);
+
+/* Norm, weight [dim] (NULL: ones; shared by the heads) and rotation in one
+ * pass; in place as above.  freq may be NULL where rotary is 0. */
+gdn2_status gdn2_qk_norm_fwd(const gdn2_rotary_desc *desc, const void *q, const void *k, const void *q_weight,
+                             const void *k_weight, const double *freq, const int32_t *positions, void *q_out,
+                             void *k_out, void *stream);
+
+/* Device workspace, in bytes, for the sums of gdn2_qk_norm_bwd. */
+gdn2_status gdn2_qk_norm_bwd_workspace(const gdn2_rotary_desc *desc, size_t *bytes);
+
+/* Gradients of <d_q_out, q_out> + <d_k_out, k_out>: dq, dk (contiguous) and
+ * d_q_weight, d_k_weight [dim] (either may be NULL), summed in a fixed order.
+ * q, k are the forward's inputs.  The workspace (256-byte aligned) may be NULL
+ * when both weight gradients are.  Outputs overlap nothing else.  No tokens:
+ * the weight gradients are 0. */
+gdn2_status gdn2_qk_norm_bwd(const gdn2_rotary_desc *desc, const void *d_q_out, const void *d_k_out, const void *q,
+                             const void *k, const void *q_weight, const void *k_weight, const double *freq,
+                             const int32_t *positions, void *dq, void *dk, void *d_q_weight, void *d_k_weight,
+                             void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A gated linear recurrence over channels, the mixer whose state is one value
+ * a channel (linear attention without a key axis):
+ *
+ *     h_t = a_t h_{t-1} + w_t x_t,   y_t = h_t,   a_t = exp(log_decay_t)
+ *
+ * for each of `dim` channels, with w = 1, or w = 1 - a (desc->complement).
+ * With desc->gate_logits the gate holds logits g instead: log a = -softplus(g)
+ * as elsewhere in this file, so a = sigmoid(-g), 1 - a = sigmoid(g), and the
+ * gradient is that of the logits.
+ *
+ * x, y [B,T,dim] (dtype), log_decay [B,T,dim] (gate_dtype), states [B,dim]
+ * fp32.  Products, sums and states are fp32 in a fixed order, so results are
+ * the same, bit for bit, on every run; results of fewer bits are rounded once.
+ *
+ * For the backward, the forward leaves the state that enters every 128th
+ * token (its marks): [B, ceil(T/128), dim] fp32, row j the state that token
+ * 128 j multiplies by its decay (token 0: the initial state).  Packed:
+ * [ceil(T/128), dim], counted along the packed axis.
+ *
+ * Preconditions not checked: all values finite, log_decay <= 0 (minus infinity
+ * is allowed and clears the state).
+ *
+ * GDN2_ERR_UNSUPPORTED: a sequence of 2^31 tokens or more, 2^31 or more
+ * sequences or channels, 2^24 or more blocks of 64 channels over all sequences
+ * (packed: over the axis), or 2^31 or more of their tiles of 128 tokens.
+ */
+typedef struct gdn2_scan_desc {
+    int64_t batch;       /* B >= 0 (packed: N sequences)            */
+    int64_t seqlen;      /* T >= 0 (packed: tokens of the one axis) */
+    int64_t dim;         /* channels >= 1 */
+    int32_t dtype;       /* gdn2_dtype of x, y and their gradients */
+    int32_t gate_dtype;  /* gdn2_dtype of log_decay and its gradient */
+    int32_t gate_logits; /* nonzero: log_decay holds logits */
+    int32_t complement;  /* nonzero: w = 1 - a, else w = 1 */
+} gdn2_scan_desc;
+
+/* Device workspace, in bytes, for gdn2_scan_fwd; 0 where it needs none. */
+gdn2_status gdn2_scan_fwd_workspace(const gdn2_scan_desc *desc, size_t *bytes);
+
+/*
+ * Forward over whole sequences.
+ *   state0     [B,dim] fp32, or NULL for zeros
+ *   y          [B,T,dim]
+ *   state_out  [B,dim] fp32, or NULL; it may be exactly state0
+ *   marks      see above, or NULL
+ *   workspace  >= gdn2_scan_fwd_workspace() bytes, 256-byte aligned, its
+ *              contents undefined before and after; NULL where that is 0.
+ *              Calls that share one must not overlap in time.
+ * Outputs overlap nothing else.  T == 0: state_out receives state0 (or zeros).
+ */
+gdn2_status gdn2_scan_fwd(const gdn2_scan_desc *desc, const void *x, const void *log_decay, const float *state0,
+                          void *y, float *state_out, float *marks, void *workspace, size_t ws_bytes, void *stream);
+
+gdn2_status gdn2_scan_fwd_varlen_workspace(const gdn2_scan_desc *desc, size_t *bytes);
+
+/* The forward over N = desc->batch sequences packed along one axis of T
+ * tokens: x, log_decay, y [T,dim], states [N,dim], cu_seqlens as for
+ * gdn2_linear_fwd_varlen (clamped, so no access leaves the buffers).  Rows of
+ * y, and of marks, outside every sequence are untouched; an empty sequence
+ * passes its state through. */
+gdn2_status gdn2_scan_fwd_varlen(const gdn2_scan_desc *desc, const int32_t *cu_seqlens, const void *x,
+                                 const void *log_decay, const float *state0, void *y, float *state_out, float *marks,
+                                 void *workspace, size_t ws_bytes, void *stream);
+
+gdn2_status gdn2_scan_bwd_workspace(const gdn2_scan_desc *desc, size_t *bytes);
+
+/*
+ * Backward of gdn2_scan_fwd: the gradients of <dy, y> + <d_state_out, h_T>.
+ *   marks        as the forward left them
+ *   state0       the forward's, or NULL for zeros
+ *   d_state_out  [B,dim] fp32, or NULL for zeros
+ *   dx           like x;  d_log_decay like log_decay
+ *   d_state0     [B,dim] fp32, or NULL to skip
+ * Outputs overlap nothing else.  T == 0: d_state0 receives d_state_out (or
+ * zeros).
+ */
+gdn2_status gdn2_scan_bwd(const gdn2_scan_desc *desc, const void *dy, const void *x, const void *log_decay,
+                          const float *marks, const float *state0, const float *d_state_out, void *dx,
+                          void *d_log_decay, float *d_state0, void *workspace, size_t ws_bytes, void *stream);
+
+gdn2_status gdn2_scan_bwd_varlen_workspace(const gdn2_scan_desc *desc, size_t *bytes);
+
+/* Backward of gdn2_scan_fwd_varlen; rows of dx and d_log_decay outside every
+ * sequence are untouched. */
+gdn2_status gdn2_scan_bwd_varlen(const gdn2_scan_desc *desc, const int32_t *cu_seqlens, const void *dy, const void *x,
+                                 const void *log_decay, const float *marks, const float *state0,
+                                 const float *d_state_out, void *dx, void *d_log_decay, float *d_state0,
+                                 void *workspace, size_t ws_bytes, void *stream);
+
+/* One decode step for N = desc->batch sequences (desc->seqlen must be 1): x,
+ * log_decay, y [N,dim]; state [N,dim] fp32 is read and rewritten in place.  y
+ * overlaps nothing else. */
+gdn2_status gdn2_scan_step(const gdn2_scan_desc *desc, const void *x, const void *log_decay, float *state, void *y,
+                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif
