@@ -26,7 +26,7 @@ struct ScanArgs {
 };
 
 bool scan_fits(const ScanArgs &a);  // whether the launches of a request stay in range
-size_t scan_workspace(const ScanArgs &a, bool backward);
+size_t scan_workspace(const ScanArgs &a);
 hipError_t launch_scan_fwd(const ScanArgs &a, void *ws, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs &a, void *ws, hipStream_t s);
 

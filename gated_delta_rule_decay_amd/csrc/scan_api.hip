@@ -56,18 +56,18 @@ Bytes bytes_of(const gdn2_scan_desc *d, bool packed) {
     return b;
 }
 
-gdn2_status space_of(const gdn2_scan_desc *d, bool packed, bool backward, size_t *bytes) {
+gdn2_status space_of(const gdn2_scan_desc *d, bool packed, size_t *bytes) {
     if (!bytes) return GDN2_ERR_NULL;
     const gdn2_status st = check(d, packed);
     if (st != GDN2_OK) return st;
-    *bytes = gdn2::scan_workspace(args_of(d, packed ? &packed_mark : nullptr, nullptr, nullptr, nullptr), backward);
+    *bytes = gdn2::scan_workspace(args_of(d, packed ? &packed_mark : nullptr, nullptr, nullptr, nullptr));
     return GDN2_OK;
 }
 
 gdn2_status forward(const gdn2_scan_desc *d, bool packed, const int32_t *cu, const void *x, const void *gate, const float *s0,
                     void *y, float *s_out, float *marks, void *ws, size_t ws_bytes, void *stream) {
     size_t need = 0;
-    const gdn2_status st = space_of(d, packed, false, &need);
+    const gdn2_status st = space_of(d, packed, &need);
     if (st != GDN2_OK) return st;
     const bool work = d->batch > 0 && d->seqlen > 0;
     if (packed && d->batch > 0 && !cu) return GDN2_ERR_NULL;
@@ -93,7 +93,7 @@ gdn2_status backward(const gdn2_scan_desc *d, bool packed, const int32_t *cu, co
                      const float *marks, const float *s0, const float *d_sT, void *dx, void *d_gate, float *d_s0, void *ws,
                      size_t ws_bytes, void *stream) {
     size_t need = 0;
-    const gdn2_status st = space_of(d, packed, true, &need);
+    const gdn2_status st = space_of(d, packed, &need);
     if (st != GDN2_OK) return st;
     const bool work = d->batch > 0 && d->seqlen > 0;
     if (packed && d->batch > 0 && !cu) return GDN2_ERR_NULL;
@@ -119,10 +119,10 @@ gdn2_status backward(const gdn2_scan_desc *d, bool packed, const int32_t *cu, co
 
 extern "C" {
 
-gdn2_status gdn2_scan_fwd_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, false, false, bytes); }
-gdn2_status gdn2_scan_fwd_varlen_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, true, false, bytes); }
-gdn2_status gdn2_scan_bwd_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, false, true, bytes); }
-gdn2_status gdn2_scan_bwd_varlen_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, true, true, bytes); }
+gdn2_status gdn2_scan_fwd_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, false, bytes); }
+gdn2_status gdn2_scan_fwd_varlen_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, true, bytes); }
+gdn2_status gdn2_scan_bwd_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, false, bytes); }
+gdn2_status gdn2_scan_bwd_varlen_workspace(const gdn2_scan_desc *d, size_t *bytes) { return space_of(d, true, bytes); }
 
 gdn2_status gdn2_scan_fwd(const gdn2_scan_desc *d, const void *x, const void *log_decay, const float *state0, void *y,
                           float *state_out, float *marks, void *workspace, size_t ws_bytes, void *stream) {

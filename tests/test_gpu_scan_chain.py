@@ -1,0 +1,106 @@
+"""The gated scan over chains of many tiles, whose states pass between
+workgroups."""
+import pytest
+import torch
+
+from tests import scan_oracle as ref
+from tests.test_gpu_scan import BF, F32, both, check_backward, check_forward, dev, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def g():
+    import gated_delta_rule_decay_amd as pkg
+    return pkg
+
+
+# 1 to 3 tiles, the 15th to 17th (a state is left behind the 16th), and the 33rd
+@pytest.mark.parametrize("tiles", [2, 3, 15, 16, 17, 32, 33, 50])
+@pytest.mark.parametrize("D", [64, 72, 3])
+def test_tiles(g, tiles, D):
+    for T in (128 * tiles, 128 * tiles - 127, 128 * tiles - 5):
+        d = make(1, T, D, seed=tiles, state=T % 2 == 1)
+        y, S, marks, r = both(g, d, False, False)
+        check_forward(d, y, S, marks, False, False)
+        check_backward(d, r, False, False)
+
+
+@pytest.mark.parametrize("N,D", [(1, 1), (7, 64), (9, 64), (3, 200), (20, 130)])
+def test_chains(g, N, D):
+    # fewer chains than counters, and numbers that leave them unequal shares
+    d = make(N, 2500, D, BF, BF, True, seed=N)
+    y, S, marks, r = both(g, d, True, True)
+    check_forward(d, y, S, marks, True, True)
+    check_backward(d, r, True, True)
+
+
+def test_long_memories_across_tiles(g):
+    # decays next to 1: every tile's state reaches the end
+    for comp in (False, True):
+        d = make(1, 5000, 16, seed=1)
+        d["gate"] = -torch.rand(d["gate"].shape, generator=torch.Generator().manual_seed(1)) * 2e-4
+        y, S, marks, r = both(g, d, False, comp)
+        check_forward(d, y, S, marks, False, comp)
+        check_backward(d, r, False, comp)
+
+
+def test_many_sequences_over_many_tiles(g):
+    gen = torch.Generator().manual_seed(2)
+    lens = [int(n) for n in torch.randint(0, 300, (30,), generator=gen)] + [2500, 1, 1, 700]
+    d = make(len(lens), sum(lens), 72, BF, packed=True, seed=3)
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).int().cuda()
+    y, S, marks, r = both(g, d, False, True, cu)
+    check_forward(d, y, S, marks, False, True, lens)
+    check_backward(d, r, False, True, lens)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_state_in_place_over_many_tiles(g, packed):
+    lens = [3000, 0, 1500, 7, 900]
+    N, T = (len(lens), sum(lens)) if packed else (3, 2600)
+    d = dev(make(N, T, 64, BF, packed=packed, seed=4))
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).int().cuda()
+    call = (lambda st, out: g.gated_scan_fwd_varlen(d["x"], d["gate"], cu, st, state_out=out, return_marks=True)) if packed else (
+        lambda st, out: g.gated_scan_fwd(d["x"], d["gate"], st, state_out=out, return_marks=True))
+    y, S, m = call(d["s0"], None)
+    for _ in range(5):
+        st = d["s0"].clone()
+        y2, _, m2 = call(st, st)
+        assert torch.equal(y, y2) and torch.equal(S, st) and torch.equal(m, m2)
+
+
+def test_same_bits_every_time(g):
+    d = make(2, 6000, 256, F32, seed=5)
+    first = both(g, d, False, False)
+    for _ in range(5):
+        again = both(g, d, False, False)
+        assert all(torch.equal(a, b) for a, b in zip(first[:3], again[:3]))
+        assert all(torch.equal(first[3][n], again[3][n]) for n in first[3])
+
+
+def test_two_streams_with_their_own_workspaces(g):
+    ds = [dev(make(2, 4000, 512, BF, seed=i)) for i in range(2)]
+    want = [g.gated_scan_fwd(d["x"], d["gate"], d["s0"])[0] for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    for _ in range(4):
+        got = []
+        for d, s in zip(ds, streams):
+            with torch.cuda.stream(s):
+                got.append(g.gated_scan_fwd(d["x"], d["gate"], d["s0"])[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_one_workspace_for_many_calls(g):
+    from gated_delta_rule_decay_amd.scan import make_scan_desc
+    n = max(g.gated_scan_fwd_workspace(make_scan_desc(2, 3000, 128)), g.gated_scan_bwd_workspace(make_scan_desc(1, 5000, 64)))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    for N, T, D in ((2, 3000, 128), (1, 5000, 64), (2, 300, 16), (2, 3000, 128)):
+        d = dev(make(N, T, D, BF, seed=T))
+        y, S, m = g.gated_scan_fwd(d["x"], d["gate"], d["s0"], return_marks=True, workspace=ws)
+        r = g.gated_scan_bwd(d["dy"], d["x"], d["gate"], m, d["s0"], d["ds"], workspace=ws)
+        y2, S2, m2 = g.gated_scan_fwd(d["x"], d["gate"], d["s0"], return_marks=True)
+        r2 = g.gated_scan_bwd(d["dy"], d["x"], d["gate"], m2, d["s0"], d["ds"])
+        assert torch.equal(y, y2) and torch.equal(S, S2) and torch.equal(m, m2) and all(torch.equal(r[k], r2[k]) for k in r)
