@@ -97,12 +97,6 @@ struct Two {
     }
 };
 
-template <class T>
-__device__ __forceinline__ T from_f32(float x) {
-    if constexpr (sizeof(T) == 2) return f32_to_bf16(x);
-    else return x;
-}
-
 template <class T, int VE, bool VEC, bool INTER>
 __device__ __forceinline__ void store_two(T *row, const Place &p, int d, int rot, const float (&a)[VE], const float (&b)[VE]) {
     if constexpr (VEC) {

@@ -1,0 +1,246 @@
+// scan_bwd.hip -- gradients of the gated scan, see scan_tile.h.
+#include "scan_tile.h"
+
+namespace gdn2 {
+namespace scan {
+namespace {
+
+constexpr int NTH = 256;  // lanes of a workgroup where each holds 8 channels
+
+template <class T, class G, int VE, int FORM, bool PACKED>
+__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 3) : 4) scan_bwd_kernel(ScanArgs a, Chain ch) {
+    using Q = Lanes<VE, NTH>;
+    constexpr int K = Q::K, PARTS = Q::PARTS;
+    __shared__ float2 s_map[Q::GRP][CW], s_rev[Q::GRP][CW];
+    __shared__ float2 s_part[PARTS][CW], s_rpart[PARTS][CW], s_look[PARTS][CW];
+    __shared__ float s_start[CW];
+    __shared__ int s_tile;
+    const int blocks = static_cast<int>((a.D + CW - 1) / CW), states = PACKED ? static_cast<int>(a.N) : 1;
+    const int l = threadIdx.x % Q::LPR, g = threadIdx.x / Q::LPR;
+    const int jc = threadIdx.x % CW, jp = __builtin_amdgcn_readfirstlane(threadIdx.x / CW);
+    const unsigned D = static_cast<unsigned>(a.D);
+    const Form<FORM> form(a);
+    // packed: the states of the sequences
+    const auto b0 = buffer<float>(a.s0, 0, PACKED && a.s0 ? states * D : 0), bd = buffer<float>(a.d_sT, 0, PACKED && a.d_sT ? states * D : 0);
+
+    if (threadIdx.x == 0) s_tile = next_tile(ch, true);
+    __syncthreads();
+    int tile = __builtin_amdgcn_readfirstlane(s_tile);
+    while (tile >= 0) {
+        const int next = jp == 0 ? take(ch, false) : 0;
+        // steps of a chain go from its last tile to its first
+        const Spot p = spot_of<PACKED>(ch, a.T, blocks, tile, true);
+        const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
+        const int64_t base = p.row * a.D;
+        auto at = [&](int k, unsigned size) { return (c < D ? lane * size : NOWHERE) + k * D * size; };
+        Row<T, VE> x[K], dy[K];
+        float V[K][VE];  // decays, see small_of_log
+        Rows<K, PACKED> rw;
+        // the state that enters the tile, and the gradient that enters the chain
+        float h = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.marks, p.mark * a.D, D), 4 * (p.cb + jc), 0, 0));
+        float r0 = 0.f, r = 0.f;
+        if (!PACKED && p.step == 0 && jp == 0)
+            r0 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.d_sT, p.sequence * a.D, a.d_sT ? D : 0), 4 * (p.cb + jc), 0, 0));
+        {
+            Row<G, VE> gt[K];
+            const auto bx = buffer<T>(a.x, base, p.rows * D), bg = buffer<G>(a.gate, base, p.rows * D), by = buffer<T>(a.dy, base, p.rows * D);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                x[k].load(bx, at(k, sizeof(T)));
+                gt[k].load(bg, at(k, sizeof(G)));
+                dy[k].load(by, at(k, sizeof(T)));
+            }
+            rw.read(ch.seq, p.row, g * K, p.rows);
+            auto gates = [&](auto f) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        V[k][e] = f(gt[k][e]);
+                        settle(V[k][e]);
+                    }
+            };
+            if (form.logits) gates([](float y) { return small_of_logit(y); });
+            else gates([](float y) { return small_of_log(y); });
+        }
+        {
+            // maps of the group: forward (fa, fu), backward (ra, ru)
+            float fa[VE], fu[VE], ra[VE], ru[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                fa[e] = ra[e] = 1.f;
+                fu[e] = ru[e] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float h0[VE], d0[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) h0[e] = d0[e] = 0.f;
+                if (PACKED && rw.edges) {
+                    Row<float, VE> i, o;
+                    i.load(b0, rw.state(k, rw.first(k), D, c4));
+                    o.load(bd, rw.state(k, rw.last(k), D, c4));
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        h0[e] = i[e];
+                        d0[e] = o[e];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float f = rw.live(k) ? decay_of(V[k][e]) : 1.f;
+                    float u = form.comp ? rest_of(V[k][e]) * x[k][e] : x[k][e], y = dy[k][e];
+                    if (PACKED) {
+                        u += f * h0[e];
+                        y += d0[e];
+                    }
+                    u = rw.live(k) ? u : 0.f;
+                    y = rw.live(k) ? y : 0.f;
+                    const float in = rw.first(k) ? 0.f : f;
+                    fu[e] = in * fu[e] + u;
+                    fa[e] *= in;
+                    // from right to left: the tokens so far come after this one's r
+                    ru[e] += ra[e] * (f * y);
+                    ra[e] = rw.last(k) ? 0.f : ra[e] * f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                s_map[g][l * VE + e] = make_float2(fa[e], fu[e]);
+                s_rev[g][l * VE + e] = make_float2(ra[e], ru[e]);
+            }
+        }
+        __syncthreads();
+        if (jp == 0) s_tile = __builtin_amdgcn_readfirstlane(next);
+        {
+            float2 m = make_float2(1.f, 0.f), n = make_float2(1.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < Q::PER; ++i) {
+                const float2 f = s_map[jp * Q::PER + i][jc], b = s_rev[jp * Q::PER + i][jc];
+                m = make_float2(f.x * m.x, f.x * m.y + f.y);
+                n = make_float2(n.x * b.x, n.x * b.y + n.y);
+            }
+            s_part[jp][jc] = m;
+            s_rpart[jp][jc] = n;
+        }
+        __syncthreads();
+        tile = __builtin_amdgcn_readfirstlane(s_tile);
+        if (ch.tiles > 1) {
+            if (jp == 0 && p.step + 1 < ch.tiles) {
+                float2 n = s_rpart[0][jc];
+#pragma unroll
+                for (int i = 1; i < PARTS; ++i) n = make_float2(n.x * s_rpart[i][jc].x, n.x * s_rpart[i][jc].y + n.y);
+                if (p.step == 0) n = make_float2(0.f, n.x * r0 + n.y);
+                leave(ch.maps + (p.chain * ch.tiles + p.step) * CW + jc, n.x, n.y);
+            }
+            s_look[jp][jc] = look_back<Q::LOOK>(ch, p.chain, p.step, jc, jp, r0, r);
+            if (jp == 0) s_start[jc] = r;
+            __syncthreads();
+            r = s_start[jc];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) r = s_look[i][jc].x * r + s_look[i][jc].y;
+        } else {
+            if (jp == 0) s_start[jc] = r0;
+            __syncthreads();
+            r = s_start[jc];
+        }
+        for (int i = 0; i < jp; ++i) h = s_part[i][jc].x * h + s_part[i][jc].y;
+        for (int i = PARTS - 1; i > jp; --i) r = s_rpart[i][jc].x * r + s_rpart[i][jc].y;
+#pragma unroll
+        for (int i = 0; i < Q::PER; ++i) {
+            float2 &m = s_map[jp * Q::PER + i][jc];
+            const float next_h = m.x * h + m.y;
+            m.y = h;
+            h = next_h;
+        }
+#pragma unroll
+        for (int i = Q::PER - 1; i >= 0; --i) {
+            float2 &m = s_rev[jp * Q::PER + i][jc];
+            const float next_r = m.x * r + m.y;
+            m.y = r;
+            r = next_r;
+        }
+        if (jp == 0 && p.step % STRIDE == STRIDE - 1 && p.step + 1 < ch.tiles)
+            leave(ch.states + (p.chain * (ch.tiles / STRIDE) + p.step / STRIDE) * CW + jc, 0.f, r);
+        __syncthreads();
+        // decoded again below: a and w of all tokens would not fit beside the states
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) settle(V[k][e]);
+        const auto bdx = buffer<T>(a.dx, base, p.rows * D), bdg = buffer<G>(a.d_gate, base, p.rows * D);
+        float H[K][VE], rv[VE];  // H: the states that enter the tokens
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            H[0][e] = s_map[g][l * VE + e].y;
+            rv[e] = s_rev[g][l * VE + e].y;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (PACKED && rw.edges) {
+                Row<float, VE> i;
+                i.load(b0, rw.state(k, rw.first(k), D, c4));
+#pragma unroll
+                for (int e = 0; e < VE; ++e) H[k][e] = rw.first(k) ? i[e] : H[k][e];
+            }
+            if (k + 1 < K)
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    H[k + 1][e] = decay_of(V[k][e]) * H[k][e] + (form.comp ? rest_of(V[k][e]) * x[k][e] : x[k][e]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) settle(V[k][e]);
+        const bool starts = a.d_s0 != nullptr && (PACKED ? rw.edges : p.step == ch.tiles - 1 && jp == 0);
+        const auto bs = PACKED ? buffer<float>(a.d_s0, 0, states * D) : buffer<float>(a.d_s0, p.sequence * a.D, D);
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            float gx[VE], gl[VE];
+            if (PACKED && rw.edges) {
+                Row<float, VE> o;
+                o.load(bd, rw.state(k, rw.last(k), D, c4));
+#pragma unroll
+                for (int e = 0; e < VE; ++e) rv[e] = rw.last(k) ? o[e] : rv[e];
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float w = rest_of(V[k][e]), s = dy[k][e] + rv[e];
+                rv[e] = rw.live(k) ? decay_of(V[k][e]) * s : rv[e];
+                gx[e] = form.comp ? w * s : s;
+                gl[e] = rv[e] * (H[k][e] - (form.comp ? x[k][e] : 0.f));
+                if (form.logits) gl[e] *= -w;
+            }
+            store_row<T, VE>(bdx, rw.live(k) ? at(k, sizeof(T)) : NOWHERE, gx);
+            store_row<G, VE>(bdg, rw.live(k) ? at(k, sizeof(G)) : NOWHERE, gl);
+            if (starts) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.first(k), D, c4) : g * K + k == 0 ? c4 : NOWHERE, rv);
+        }
+    }
+}
+
+}  // namespace
+}  // namespace scan
+
+using namespace scan;
+
+// workgroups that run at once
+constexpr int AT_ONCE = 768;
+
+hipError_t launch_scan_bwd(const ScanArgs &a, void *ws, hipStream_t s) {
+    Chain ch = {};
+    const hipError_t e = prepare(a, ws, a.d_sT, a.d_s0, ch, s);
+    if (e != hipSuccess) return e;
+    const bool vec = a.D % 8 == 0 && aligned(a.x) && aligned(a.gate) && aligned(a.dy) && aligned(a.dx) && aligned(a.d_gate) &&
+                     aligned(a.marks) && aligned(a.s0) && aligned(a.d_sT) && aligned(a.d_s0);
+    return by_kind(a, vec, [&](auto t, auto g, auto ve, auto form) {
+        using T = decltype(t);
+        using G = decltype(g);
+        constexpr int VE = decltype(ve)::value, FORM = decltype(form)::value;
+        const dim3 grid(grid_of(ch, AT_ONCE)), block(Lanes<VE, NTH>::NTH);
+        if (a.cu) hipLaunchKernelGGL((scan_bwd_kernel<T, G, VE, FORM, true>), grid, block, 0, s, a, ch);
+        else hipLaunchKernelGGL((scan_bwd_kernel<T, G, VE, FORM, false>), grid, block, 0, s, a, ch);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace gdn2
