@@ -15,8 +15,9 @@
 // Angles: p f / 2 pi in fp64 (53 bits; a position of 2^20 leaves 2^-33 turns),
 // the nearest quarter turn taken off exactly, then the Taylor series of sine
 // and cosine on [-pi/4, pi/4] in fp32, whose first terms left out are below
-// 2^-28.  The sum of squares and its root are fp64, so no row of finite values
-// overflows or vanishes; everything else is fp32, rounded once.
+// 2^-28.  Everything else is fp32, rounded once at the end; a row whose sum of
+// squares leaves [2^-80, 2^100] is summed and scaled in fp64 instead, so that no
+// row of finite values overflows or vanishes.
 #include <type_traits>
 
 #include "common.h"
@@ -27,7 +28,8 @@ namespace gdn2 {
 namespace {
 
 constexpr int NTH = 256;
-constexpr int ROUNDS = 4;       // rows of a lane group in one go
+// rows of a lane group in one go: what the registers hold of x, or of x and dy
+constexpr int rounds_of(int mode) { return mode == ROTARY_NORM_BWD ? 2 : 4; }
 constexpr int MAX_TOKENS = 16;  // tokens of a workgroup
 constexpr int MAX_PAIRS = 128;
 
@@ -78,16 +80,18 @@ __device__ __forceinline__ bool own1(const Place &p, int e, int d, int rot) {
     return p.turn ? (INTER ? p.c1 + e < rot : p.c1 + e < rot) : p.c1 + e < d;
 }
 
+// A row's two vectors of a lane.  VEC: `b` and `at` give its first element, and
+// what is not the lane's reads as zero; else `row` does.
 template <class T, int VE, bool VEC, bool INTER>
 struct Two {
     Pack<T, VE> a, b;
-    __device__ __forceinline__ void load(const T *row, const Place &p, int d, int rot, bool on) {
-        a = b = Pack<T, VE>{};
-        if (!on) return;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, unsigned at, const T *row, const Place &p, int d, int rot, bool on) {
         if constexpr (VEC) {
-            a = *reinterpret_cast<const Pack<T, VE> *>(row + p.c0);
-            if (p.c1 < d) b = *reinterpret_cast<const Pack<T, VE> *>(row + p.c1);
+            a = __builtin_bit_cast(Pack<T, VE>, __builtin_amdgcn_raw_buffer_load_b128(buf, on ? at + p.c0 * static_cast<unsigned>(sizeof(T)) : NOWHERE, 0, 0));
+            b = __builtin_bit_cast(Pack<T, VE>, __builtin_amdgcn_raw_buffer_load_b128(buf, on && p.c1 < d ? at + p.c1 * static_cast<unsigned>(sizeof(T)) : NOWHERE, 0, 0));
         } else {
+            a = b = Pack<T, VE>{};
+            if (!on) return;
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 if (own0<INTER>(p, e, d, rot)) a.e[e] = row[p.c0 + e];
@@ -98,18 +102,19 @@ struct Two {
 };
 
 template <class T, int VE, bool VEC, bool INTER>
-__device__ __forceinline__ void store_two(T *row, const Place &p, int d, int rot, const float (&a)[VE], const float (&b)[VE]) {
+__device__ __forceinline__ void store_two(__amdgpu_buffer_rsrc_t buf, unsigned at, T *row, const Place &p, int d, int rot, bool on,
+                                          const float (&a)[VE], const float (&b)[VE]) {
     if constexpr (VEC) {
-        Pack<T, VE> u;
+        Pack<T, VE> u, v;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) u.e[e] = from_f32<T>(a[e]);
-        *reinterpret_cast<Pack<T, VE> *>(row + p.c0) = u;
-        if (p.c1 < d) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) u.e[e] = from_f32<T>(b[e]);
-            *reinterpret_cast<Pack<T, VE> *>(row + p.c1) = u;
+        for (int e = 0; e < VE; ++e) {
+            u.e[e] = from_f32<T>(a[e]);
+            v.e[e] = from_f32<T>(b[e]);
         }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, u), buf, on ? at + p.c0 * static_cast<unsigned>(sizeof(T)) : NOWHERE, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), buf, on && p.c1 < d ? at + p.c1 * static_cast<unsigned>(sizeof(T)) : NOWHERE, 0, 0);
     } else {
+        if (!on) return;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             if (own0<INTER>(p, e, d, rot)) row[p.c0 + e] = from_f32<T>(a[e]);
@@ -146,19 +151,26 @@ struct Shape {
     int tokens[2];  // of a workgroup, for q and k
     int64_t tiles[2];
     int grid[2];    // workgroups of q and k
+    unsigned by_heads[2], by_pairs;  // see quotient()
 };
 
+// n / d for n < 2^16 from m = ceil(2^32 / d), d < 2^16: m d - 2^32 < d, so the
+// error n (m d - 2^32) / (2^32 d) stays below 1 / d.  d = 1: m = 0.
+__device__ __forceinline__ int quotient(unsigned n, unsigned m) { return m ? __umulhi(n, m) : n; }
+
 template <class T, int VE, bool VEC, bool INTER, int MODE>
-__global__ void __launch_bounds__(NTH) rotary_kernel(RotaryArgs a, Shape sh, float *part) {
+__global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4) rotary_kernel(RotaryArgs a, Shape sh, float *part) {
+    constexpr int ROUNDS = rounds_of(MODE);
     __shared__ float s_cos[MAX_TOKENS][MAX_PAIRS + 8], s_sin[MAX_TOKENS][MAX_PAIRS + 8];
     const int which = blockIdx.x >= static_cast<unsigned>(sh.grid[0]);
     const int block = which ? blockIdx.x - sh.grid[0] : blockIdx.x;
     const RotaryPart pt = a.part[which];
-    const int L = sh.lanes, l = threadIdx.x % L, slot = threadIdx.x / L, slots = NTH / L;
+    const int L = sh.lanes, l = threadIdx.x & (L - 1), slot = threadIdx.x / L, slots = NTH / L;
     const int d = a.d, rot = a.rot, half = rot / 2, H = pt.H, TT = sh.tokens[which];
     const Place p = place_of<VE, INTER>(l, d, rot);
-    const int64_t width = static_cast<int64_t>(H) * d;
     const int pairs = (half + VE - 1) / VE * VE;  // angles that some lane reads
+    const float per = a.l2 ? 1.f : 1.f / d;
+    const double offset = static_cast<double>(a.offset);  // exact, and so are its sums with positions
 
     float w0[VE], w1[VE], dw0[VE], dw1[VE];
     if constexpr (MODE != ROTARY_TURN) {
@@ -176,6 +188,9 @@ __global__ void __launch_bounds__(NTH) rotary_kernel(RotaryArgs a, Shape sh, flo
     for (int64_t tile = block; tile < sh.tiles[which]; tile += sh.grid[which]) {
         const int t0 = static_cast<int>(tile * TT), nt = a.tokens - t0 < TT ? a.tokens - t0 : TT;
         const int rows = nt * H;
+        const int64_t out = static_cast<int64_t>(t0) * H * d;  // contiguous rows
+        constexpr int ALL = 0x7fffffff / sizeof(T);
+        const auto bx = buffer<T>(pt.x, t0 * pt.stride, ALL), bdy = buffer<T>(pt.dy, out, ALL), by = buffer<T>(pt.y, out, ALL);
         for (int base = 0; base < rows; base += slots * ROUNDS) {
             Two<T, VE, VEC, INTER> x[ROUNDS], dy[MODE == ROTARY_NORM_BWD ? ROUNDS : 1];
             int tok[ROUNDS];
@@ -183,20 +198,22 @@ __global__ void __launch_bounds__(NTH) rotary_kernel(RotaryArgs a, Shape sh, flo
             for (int i = 0; i < ROUNDS; ++i) {
                 const int r = base + slot + i * slots;
                 const bool on = r < rows && p.live;
-                tok[i] = r < rows ? r / H : 0;
-                const int h = r - tok[i] * H;
-                x[i].load(static_cast<const T *>(pt.x) + (t0 + tok[i]) * pt.stride + static_cast<int64_t>(h) * d, p, d, rot, on);
+                tok[i] = r < rows ? quotient(r, sh.by_heads[which]) : 0;
+                const int at = (r - tok[i] * H) * d;
+                x[i].load(bx, (tok[i] * static_cast<unsigned>(pt.stride) + at) * sizeof(T),
+                          static_cast<const T *>(pt.x) + (t0 + tok[i]) * pt.stride + at, p, d, rot, on);
                 if constexpr (MODE == ROTARY_NORM_BWD)
-                    dy[i].load(static_cast<const T *>(pt.dy) + (t0 + tok[i]) * width + static_cast<int64_t>(h) * d, p, d, rot, on);
+                    dy[i].load(bdy, r * d * static_cast<unsigned>(sizeof(T)), static_cast<const T *>(pt.dy) + out + r * d, p, d, rot, on);
             }
             if (base == 0) {
                 __syncthreads();  // the last tile's readers
+                const int first = t0 % a.period;
                 for (int i = threadIdx.x; i < nt * pairs; i += NTH) {
-                    const int t = i / pairs, j = i - t * pairs;
-                    const int at = (t0 + t) % a.period;
-                    const int64_t pos = a.offset + (a.pos ? a.pos[at] : at);
+                    const int t = quotient(i, sh.by_pairs), j = i - t * pairs;
+                    int at = first + t;
+                    if (at >= a.period) at = a.period < MAX_TOKENS ? at % a.period : at - a.period;
                     float c = 0.f, s = 0.f;  // behind the last pair
-                    if (j < half) cos_sin_turns(static_cast<double>(pos) * (a.freq[j] * 0.15915494309189535), c, s);
+                    if (j < half) cos_sin_turns((offset + (a.pos ? a.pos[at] : at)) * (a.freq[j] * 0.15915494309189535), c, s);
                     s_cos[t][j] = a.cos_mag * c;
                     s_sin[t][j] = a.sin_mag * s;
                 }
@@ -212,18 +229,48 @@ __global__ void __launch_bounds__(NTH) rotary_kernel(RotaryArgs a, Shape sh, flo
                     u[e] = to_f32<T>(x[i].a.e[e]);
                     v[e] = to_f32<T>(x[i].b.e[e]);
                 }
-                double rs = 0.0;
+                float rs = 0.f;
+                double wide = 0.0;
+                bool far = false;
                 if constexpr (MODE != ROTARY_TURN) {
-                    double ss = 0.0;
+                    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) ss += static_cast<double>(u[e]) * u[e] + static_cast<double>(v[e]) * v[e];
+                    for (int e = 0; e < VE; e += 2) {
+                        s0 += u[e] * u[e];
+                        s1 += u[e + 1] * u[e + 1];
+                        s2 += v[e] * v[e];
+                        s3 += v[e + 1] * v[e + 1];
+                    }
+                    float ss = (s0 + s1) + (s2 + s3);
                     for (int o = L >> 1; o >= 1; o >>= 1) ss += __shfl_xor(ss, o);
-                    const double m = a.l2 ? ss : ss / d + a.eps;
-                    rs = m > 0.0 ? 1.0 / sqrt(m) : 0.0;
+                    // outside, squares of fp32 overflow, or vanish beside what they add up to
+                    far = r < rows && !(ss > 0x1p-80f && ss < 0x1p100f);
+                    const float m = a.l2 ? ss : ss * per + a.eps;
+                    rs = __builtin_amdgcn_rsqf(m);
+                    rs = m > 0.f ? rs * (1.5f - 0.5f * m * rs * rs) : 0.f;  // 0: no row
+                    if (__builtin_amdgcn_ballot_w64(far) != 0) {
+                        double sum = 0.0;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        u[e] = static_cast<float>(u[e] * rs);
-                        v[e] = static_cast<float>(v[e] * rs);
+                        for (int e = 0; e < VE; ++e) {
+                            sum += static_cast<double>(u[e]) * u[e] + static_cast<double>(v[e]) * v[e];
+                            asm volatile("" : "+v"(sum));  // not all elements in 64 bits at once
+                        }
+                        for (int o = L >> 1; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+                        sum = a.l2 ? sum : sum / d + a.eps;
+                        wide = sum > 0.0 ? 1.0 / sqrt(sum) : 0.0;
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            u[e] = far ? static_cast<float>(u[e] * wide) : u[e] * rs;
+                            v[e] = far ? static_cast<float>(v[e] * wide) : v[e] * rs;
+                            settle(u[e]);
+                            settle(v[e]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            u[e] *= rs;
+                            v[e] *= rs;
+                        }
                     }
                 }
                 const float *c = &s_cos[tok[i]][p.turn ? p.j : 0], *s = &s_sin[tok[i]][p.turn ? p.j : 0];
@@ -244,11 +291,26 @@ __global__ void __launch_bounds__(NTH) rotary_kernel(RotaryArgs a, Shape sh, flo
                         dot += g[e] * u[e] + f[e] * v[e];
                     }
                     for (int o = L >> 1; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
-                    if (!a.l2) dot /= d;
+                    dot *= per;
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
-                        u[e] = static_cast<float>(rs * (g[e] - u[e] * dot));
-                        v[e] = static_cast<float>(rs * (f[e] - v[e] * dot));
+                        u[e] = g[e] - u[e] * dot;
+                        v[e] = f[e] - v[e] * dot;
+                    }
+                    if (__builtin_amdgcn_ballot_w64(far) != 0) {
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            u[e] = far ? static_cast<float>(u[e] * wide) : u[e] * rs;
+                            v[e] = far ? static_cast<float>(v[e] * wide) : v[e] * rs;
+                            settle(u[e]);
+                            settle(v[e]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            u[e] *= rs;
+                            v[e] *= rs;
+                        }
                     }
                 } else {
                     if constexpr (MODE == ROTARY_NORM)
@@ -259,7 +321,7 @@ __global__ void __launch_bounds__(NTH) rotary_kernel(RotaryArgs a, Shape sh, flo
                         }
                     if (p.turn) turn<VE, INTER>(u, v, c, s);
                 }
-                if (on) store_two<T, VE, VEC, INTER>(static_cast<T *>(pt.y) + (static_cast<int64_t>(t0) * H + r) * d, p, d, rot, u, v);
+                store_two<T, VE, VEC, INTER>(by, r * d * static_cast<unsigned>(sizeof(T)), static_cast<T *>(pt.y) + out + r * d, p, d, rot, on, u, v);
             }
         }
     }
@@ -298,7 +360,15 @@ __global__ void __launch_bounds__(1024) rotary_weight_kernel(RotaryArgs a, Shape
     double s = 0.0;
     if (c < a.d) {
         const float *p = part + static_cast<int64_t>(which ? sh.grid[0] : 0) * a.d + c;
-        for (int i = r; i < sh.grid[which]; i += 64) s += p[static_cast<int64_t>(i) * a.d];
+        int i = r;
+        for (; i + 448 < sh.grid[which]; i += 512) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p[static_cast<int64_t>(i + 64 * k) * a.d];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+        for (; i < sh.grid[which]; i += 64) s += p[static_cast<int64_t>(i) * a.d];
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
@@ -318,11 +388,14 @@ Shape shape_of(const RotaryArgs &a, int ve) {
     const int n = (a.rot / 2 + ve - 1) / ve + (a.d - a.rot + 2 * ve - 1) / (2 * ve);  // lanes with a place
     sh.lanes = 1;
     while (sh.lanes < n) sh.lanes *= 2;
-    const int slots = NTH / sh.lanes;
+    const int slots = NTH / sh.lanes, pairs = (a.rot / 2 + ve - 1) / ve * ve;
+    auto inverse = [](int64_t n) { return n > 1 ? static_cast<unsigned>(((INT64_C(1) << 32) + n - 1) / n) : 0u; };
+    sh.by_pairs = inverse(pairs);
     for (int i = 0; i < 2; ++i) {
         const int H = a.part[i].H;
         if (!H) continue;
-        int t = slots * ROUNDS / H;
+        sh.by_heads[i] = inverse(H);
+        int t = slots * rounds_of(a.mode) / H;
         t = t < 1 ? 1 : t > MAX_TOKENS ? MAX_TOKENS : t;
         sh.tokens[i] = t;
         sh.tiles[i] = (static_cast<int64_t>(a.tokens) + t - 1) / t;
@@ -333,13 +406,14 @@ Shape shape_of(const RotaryArgs &a, int ve) {
 }
 
 // Whether rows are whole aligned vectors: channels, pair blocks and strides in
-// units of VE, every pointer on 16 bytes.
+// units of VE, every pointer on 16 bytes.  Rows that are not go element by
+// element.
 bool vector_ok(const RotaryArgs &a) {
     const int ve = a.bf16 ? 8 : 4;
     if (a.d % ve || a.rot % (2 * ve)) return false;
     for (const RotaryPart &p : a.part) {
         if (!p.H) continue;
-        if (p.stride % ve) return false;
+        if (p.stride % ve || p.stride >= (1 << 24)) return false;  // 31-bit offsets within a workgroup's tokens
         for (const void *x : {p.x, p.dy, const_cast<const void *>(p.y)})
             if (reinterpret_cast<uintptr_t>(x) & 15) return false;
     }

@@ -212,21 +212,8 @@ __device__ __forceinline__ float2 look_back(const Chain &ch, int64_t chain, int 
     return m;
 }
 
-// Elements of a tensor from a uniform one on: loads behind the last read as
-// zero and stores there are dropped.  No lane of the kernels below branches by
-// itself while a tile is in registers: what a lane does not need goes to an
-// offset out of range, and branches are those of whole waves.
-template <class E>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *tensor, int64_t first, int elements) {
-    const uint64_t at = reinterpret_cast<uint64_t>(static_cast<const E *>(tensor) + first);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(static_cast<uint64_t>(hi) << 32 | lo), 0,
-                                             elements * static_cast<int>(sizeof(E)), 0x00027000);
-}
-// an offset behind every tile's end, also with a lane's rows added
-constexpr unsigned NOWHERE = 0x80000000u;
-
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+// No lane of the kernels branches by itself while a tile is in registers: what
+// a lane does not need goes to NOWHERE, and branches are those of whole waves.
 
 // VE elements of a row as stored.
 template <class E, int VE>
@@ -269,11 +256,6 @@ __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t b, unsigned at,
         }
     }
 }
-
-// Keeps the compiler from working on all elements of a lane at once, for which
-// the registers do not suffice: what follows in the program starts after `v` is
-// there (an empty instruction that is said to change it).
-__device__ __forceinline__ void settle(float &v) { asm volatile("" : "+v"(v)); }
 
 // Where a tile is.
 struct Spot {

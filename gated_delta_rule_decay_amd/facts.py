@@ -1,0 +1,41 @@
+"""Checks of tensors by what a request depends on: shape, strides, type, device.
+
+A call's checks and its descriptor follow from these alone, so they are worked
+out once for each combination (``functools.lru_cache``) and a repeated call pays
+for a look-up; addresses and contents take no part.
+"""
+from __future__ import annotations
+
+
+def facts(t):
+    """(shape, strides, dtype, device) of a tensor, None for None."""
+    if t is None:
+        return None
+    try:
+        return t.shape, t.stride(), t.dtype, t.device
+    except AttributeError:
+        raise TypeError(f"expected a torch.Tensor, not {type(t).__name__}") from None
+
+
+def contiguous(shape, stride):
+    step = 1
+    for n, s in zip(reversed(shape), reversed(stride)):
+        if n == 0:
+            return True
+        if n != 1:
+            if s != step:
+                return False
+            step *= n
+    return True
+
+
+def like(f, name, shape, dtypes, dev):
+    """Raises unless the facts are of a contiguous tensor of this shape, one of these types and device."""
+    if f[3] != dev:
+        raise ValueError(f"{name} is on {f[3]}, expected {dev}")
+    if tuple(f[0]) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(f[0])}, expected {tuple(shape)}")
+    if f[2] not in dtypes:
+        raise TypeError(f"{name} has dtype {f[2]}, expected one of {dtypes}")
+    if not contiguous(f[0], f[1]):
+        raise ValueError(f"{name} must be contiguous")

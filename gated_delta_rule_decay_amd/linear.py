@@ -72,11 +72,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(index):
-    """torch's current stream of a device, as a hipStream_t."""
+@functools.lru_cache(maxsize=1)
+def _torch_calls():
+    """The current device's index, and torch's current stream of a device as a hipStream_t."""
     import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+            stream or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 def _like(t, name, shape, dtype, dev):
@@ -91,15 +93,17 @@ def _like(t, name, shape, dtype, dev):
 
 def _run(name, dev, desc, *args):
     """Call an entry point on `dev`'s current stream; raises on a bad status."""
-    import torch
-    fn = _call(name)
+    fn = _calls.get(name) or _call(name)
     if dev.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a GPU, not on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        st = fn(desc, *args, _raw_stream(dev.index))
+    device, stream = _torch_calls()
+    index = dev.index
+    if device() == index:
+        st = fn(desc, *args, stream(index))
     else:
+        import torch
         with torch.cuda.device(dev):
-            st = fn(desc, *args, _raw_stream(dev.index))
+            st = fn(desc, *args, stream(index))
     if st != 0:
         raise Gdn2Error(st, name)
 

@@ -7,10 +7,12 @@ There is no CPU or torch fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
-from .binding import GDN2_BF16, GDN2_F32, _check
-from .linear import _dtype_code, _like, _need, _ptr, _register, _run, _space
+from .binding import GDN2_BF16, GDN2_F32
+from .facts import contiguous, facts, like
+from .linear import _bytes, _ptr, _register, _run, _space
 
 GDN2_ROTARY_HALF, GDN2_ROTARY_INTERLEAVED = 0, 1
 GDN2_QK_NONE, GDN2_QK_RMS, GDN2_QK_L2 = 0, 1, 2
@@ -72,18 +74,18 @@ def rotary_frequencies(rotary, base=10000.0, scaling=None, factor=1.0, original_
     return f.to(device)
 
 
-def _strided(t, name, tok, dtype, dev):
+def _strided(f, name, tok, dtype, dev):
     """Heads, channels and the elements between tokens of [*tok, H, d]: tokens evenly spaced, a token contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, not on {t.device}")
-    if tuple(t.shape[:-2]) != tok:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, its tokens must be {tok}")
-    H, d = t.shape[-2:]
-    if t.numel() == 0 or t.is_contiguous():
+    shape, st, dt, on = f
+    if dt != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {dt}")
+    if on != dev:
+        raise ValueError(f"{name} must be on {dev}, not on {on}")
+    if len(shape) != len(tok) + 2 or tuple(shape[:-2]) != tok:
+        raise ValueError(f"{name} has shape {tuple(shape)}, its tokens must be {tok}")
+    H, d = shape[-2:]
+    if contiguous(shape, st):
         return H, d, H * d
-    st, ok = t.stride(), True
     ok = (d == 1 or st[-1] == 1) and (H == 1 or st[-2] == d)
     step, span = None, 1  # of the innermost token axis that has more than one token
     for n, s in zip(reversed(tok), reversed(st[:-2])):
@@ -98,54 +100,72 @@ def _strided(t, name, tok, dtype, dev):
     return H, d, step
 
 
-def _plan(q, k, freq, positions, offset, interleaved, magnitude, norm, eps, weights=(None, None), names=("q", "k")):
-    """The checked request: (tokens' shape, what make_rotary_desc takes)."""
+def _type_code(dtype, name):
     import torch
-    if q.dim() < 3:
+    if dtype == torch.bfloat16:
+        return GDN2_BF16
+    if dtype == torch.float32:
+        return GDN2_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, not {dtype}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _request(names, q, k, freq, positions, q_weight, k_weight, interleaved, magnitude, norm, eps):
+    """The descriptor (offset 0) of checked facts."""
+    import torch
+    shape, _, dtype, dev = q
+    if len(shape) < 3:
         raise ValueError(f"{names[0]} is [..., H, d] with at least one token axis")
-    tok, dev = tuple(q.shape[:-2]), q.device
-    code = _dtype_code(q, names[0])
-    Hq, d, qs = _strided(q, names[0], tok, q.dtype, dev)
+    tok = tuple(shape[:-2])
+    code = _type_code(dtype, names[0])
+    Hq, d, qs = _strided(q, names[0], tok, dtype, dev)
     Hk, ks = 0, 0
     if k is not None:
-        if k.dim() != q.dim():
-            raise ValueError(f"{names[1]} must have the axes of {names[0]}")
-        Hk, dk, ks = _strided(k, names[1], tok, q.dtype, dev)
+        Hk, dk, ks = _strided(k, names[1], tok, dtype, dev)
         if dk != d:
             raise ValueError(f"{names[1]} has {dk} channels, {names[0]} has {d}")
     rot = 0
     if freq is not None:
-        if freq.dim() != 1:
+        if len(freq[0]) != 1:
             raise ValueError("freq is [rotary/2]")
-        _like(freq, "freq", freq.shape, torch.float64, dev)
-        rot = 2 * freq.numel()
+        like(freq, "freq", freq[0], (torch.float64,), dev)
+        rot = 2 * freq[0][0]
         if rot > d:
             raise ValueError(f"freq turns {rot} channels of {d}")
-    tokens = math.prod(tok)
     period = max(tok[-1], 1)  # positions count along the last token axis
     if positions is not None:
-        n = positions.dim()
-        if n < 1 or tuple(positions.shape) != tok[len(tok) - n:]:
-            raise ValueError(f"positions have shape {tuple(positions.shape)}, not {tok} or its last axes")
-        _check(positions, "positions", tuple(positions.shape), (torch.int32,), dev)
-        period = max(positions.numel(), 1)
-    wd, first = GDN2_F32, weights[0] if weights[0] is not None else weights[1]
+        n = len(positions[0])
+        if n < 1 or tuple(positions[0]) != tok[max(len(tok) - n, 0):]:
+            raise ValueError(f"positions have shape {tuple(positions[0])}, not {tok} or its last axes")
+        like(positions, "positions", positions[0], (torch.int32,), dev)
+        period = max(math.prod(positions[0]), 1)
+    wd, first = GDN2_F32, q_weight if q_weight is not None else k_weight
     if first is not None:
-        wd = _dtype_code(first, "weight")
-        for w, n in zip(weights, names):
+        wd = _type_code(first[2], "weight")
+        for w, n in ((q_weight, names[0]), (k_weight, names[1])):
             if w is not None:
-                _like(w, f"{n}_weight", (d,), first.dtype, dev)
-    return tok, (tokens, Hq, Hk, d, rot, period, qs, ks, offset, code, wd,
-                 GDN2_ROTARY_INTERLEAVED if interleaved else GDN2_ROTARY_HALF, norm, eps, magnitude)
+                like(w, f"{n}_weight", (d,), (first[2],), dev)
+    return make_rotary_desc(math.prod(tok), Hq, Hk, d, rot, period, qs, ks, 0, code, wd,
+                            GDN2_ROTARY_INTERLEAVED if interleaved else GDN2_ROTARY_HALF, norm, eps, magnitude)
+
+
+def _plan(q, k, freq, positions, offset, interleaved, magnitude, norm=GDN2_QK_NONE, eps=0.0, q_weight=None, k_weight=None,
+          names=("q", "k")):
+    """The descriptor of a checked request."""
+    desc = _request(names, facts(q), facts(k), facts(freq), facts(positions), facts(q_weight), facts(k_weight),
+                    bool(interleaved), float(magnitude), norm, float(eps))
+    if offset:  # the shared one stays as it is
+        desc = Gdn2RotaryDesc.from_buffer_copy(desc)
+        desc.offset = offset
+    return desc
 
 
 def _out(given, name, x):
-    import torch
     if x is None:
         return None
     if given is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _like(given, name, x.shape, x.dtype, x.device)
+        return x.new_empty(x.shape)
+    like(facts(given), name, x.shape, (x.dtype,), x.device)
     return given
 
 
@@ -170,18 +190,17 @@ def rotary_fwd(q, k, freq, positions=None, offset=0, interleaved=False, magnitud
     q_out, k_out: contiguous outputs, which may be q and k themselves where
     these are contiguous.  Returns (q_out, k_out).
     """
-    tok, sizes = _plan(q, k, freq, positions, offset, interleaved, magnitude, GDN2_QK_NONE, 0.0)
+    desc = _plan(q, k, freq, positions, offset, interleaved, magnitude)
     q_out, k_out = _out(q_out, "q_out", q), _out(k_out, "k_out", k)
-    _run("gdn2_rotary_fwd", q.device, make_rotary_desc(*sizes), _ptr(q), _ptr(k), _ptr(freq), _ptr(positions), _ptr(q_out), _ptr(k_out))
+    _run("gdn2_rotary_fwd", q.device, desc, _ptr(q), _ptr(k), _ptr(freq), _ptr(positions), _ptr(q_out), _ptr(k_out))
     return q_out, k_out
 
 
 def rotary_bwd(d_q_out, d_k_out, freq, positions=None, offset=0, interleaved=False, magnitude=1.0, dq=None, dk=None):
     """Gradients (dq, dk) of <d_q_out, q_out> + <d_k_out, k_out> for ``rotary_fwd``, arguments as there."""
-    tok, sizes = _plan(d_q_out, d_k_out, freq, positions, offset, interleaved, magnitude, GDN2_QK_NONE, 0.0,
-                       names=("d_q_out", "d_k_out"))
+    desc = _plan(d_q_out, d_k_out, freq, positions, offset, interleaved, magnitude, names=("d_q_out", "d_k_out"))
     dq, dk = _out(dq, "dq", d_q_out), _out(dk, "dk", d_k_out)
-    _run("gdn2_rotary_bwd", d_q_out.device, make_rotary_desc(*sizes), _ptr(d_q_out), _ptr(d_k_out), _ptr(freq), _ptr(positions),
+    _run("gdn2_rotary_bwd", d_q_out.device, desc, _ptr(d_q_out), _ptr(d_k_out), _ptr(freq), _ptr(positions),
          _ptr(dq), _ptr(dk))
     return dq, dk
 
@@ -195,16 +214,20 @@ def qk_norm_rotary_fwd(q, k, q_weight=None, k_weight=None, freq=None, positions=
     freq None: no rotation.  Other arguments as for ``rotary_fwd``.  Returns
     (q_out, k_out).
     """
-    tok, sizes = _plan(q, k, freq, positions, offset, interleaved, magnitude, _norm_code(norm), eps, (q_weight, k_weight))
+    desc = _plan(q, k, freq, positions, offset, interleaved, magnitude, _norm_code(norm), eps, q_weight, k_weight)
     q_out, k_out = _out(q_out, "q_out", q), _out(k_out, "k_out", k)
-    _run("gdn2_qk_norm_fwd", q.device, make_rotary_desc(*sizes), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(freq),
+    _run("gdn2_qk_norm_fwd", q.device, desc, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(freq),
          _ptr(positions), _ptr(q_out), _ptr(k_out))
     return q_out, k_out
 
 
 def qk_norm_rotary_bwd_workspace(desc: Gdn2RotaryDesc) -> int:
-    from .linear import _bytes
     return _bytes("gdn2_qk_norm_bwd_workspace", desc)
+
+
+@functools.lru_cache(maxsize=256)
+def _sum_bytes(tokens, q_heads, k_heads, dim, rotary, dtype):
+    return qk_norm_rotary_bwd_workspace(make_rotary_desc(tokens, q_heads, k_heads, dim, rotary, dtype=dtype, norm=GDN2_QK_RMS))
 
 
 def qk_norm_rotary_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, freq=None, positions=None, offset=0,
@@ -216,18 +239,19 @@ def qk_norm_rotary_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, fre
     there is none.  ``workspace``: None allocates it, or a uint8 device tensor
     of at least qk_norm_rotary_bwd_workspace() bytes.
     """
-    import torch
-    tok, sizes = _plan(q, k, freq, positions, offset, interleaved, magnitude, _norm_code(norm), eps, (q_weight, k_weight))
+    desc = _plan(q, k, freq, positions, offset, interleaved, magnitude, _norm_code(norm), eps, q_weight, k_weight)
     dev = q.device
-    _like(d_q_out, "d_q_out", q.shape, q.dtype, dev)
-    if k is not None:
-        _like(d_k_out, "d_k_out", k.shape, q.dtype, dev)
+    for g, x, n in ((d_q_out, q, "d_q_out"), (d_k_out, k, "d_k_out")):
+        if x is not None:
+            if g is None:
+                raise ValueError(f"{n} is missing")
+            like(facts(g), n, x.shape, (q.dtype,), dev)
     dq, dk = _out(None, "dq", q), _out(None, "dk", k)
-    dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    dqw = None if q_weight is None else q_weight.new_empty(q_weight.shape)
+    dkw = None if k_weight is None else k_weight.new_empty(k_weight.shape)
     ws, n = None, 0
     if dqw is not None or dkw is not None or workspace is not None:
-        ws, n = _space(workspace, _need("gdn2_qk_norm_bwd_workspace", make_rotary_desc, *sizes), dev)
-    _run("gdn2_qk_norm_bwd", dev, make_rotary_desc(*sizes), _ptr(d_q_out), _ptr(d_k_out) if k is not None else None, _ptr(q),
-         _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(freq), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(ws), n)
+        ws, n = _space(workspace, _sum_bytes(desc.tokens, desc.q_heads, desc.k_heads, desc.dim, desc.rotary, desc.dtype), dev)
+    _run("gdn2_qk_norm_bwd", dev, desc, _ptr(d_q_out), _ptr(d_k_out) if k is not None else None, _ptr(q), _ptr(k), _ptr(q_weight),
+         _ptr(k_weight), _ptr(freq), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(ws), n)
     return dict(dq=dq, dk=dk, d_q_weight=dqw, d_k_weight=dkw)

@@ -7,9 +7,12 @@ There is no CPU or torch fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 
-from .binding import GDN2_BF16, GDN2_F32, _check
-from .linear import _bytes, _dtype_code, _like, _need, _ptr, _register, _run, _space
+from .binding import GDN2_BF16, GDN2_F32
+from .facts import facts, like
+from .linear import _bytes, _ptr, _register, _run, _space
+from .rotary import _type_code
 
 SCAN_MARK = 128  # tokens from mark to mark
 
@@ -49,59 +52,65 @@ def gated_scan_bwd_varlen_workspace(desc: Gdn2ScanDesc) -> int:
     return _bytes("gdn2_scan_bwd_varlen_workspace", desc)
 
 
-def _sizes(x, log_decay, cu_seqlens, gate_logits, complement, step=False):
-    """(the token axes, what make_scan_desc takes) of checked inputs."""
+@functools.lru_cache(maxsize=1024)
+def _request(kind, x, log_decay, cu_seqlens, gate_logits, complement, states, *tokens):
+    """(the descriptor, workspace bytes, N, marks' shape) of checked facts.
+
+    kind: "fwd", "bwd" or "step"; states and tokens: (name, facts) pairs of
+    tensors [N,D] fp32 and of tensors like x, None among the facts skipped.
+    """
     import torch
-    if step:
-        if x.dim() != 2:
+    shape, _, dtype, dev = x
+    packed = cu_seqlens is not None
+    if kind == "step":
+        if len(shape) != 2:
             raise ValueError("x is [N,D]")
-        tok, N, T = tuple(x.shape[:1]), x.shape[0], 1
-    elif cu_seqlens is None:
-        if x.dim() != 3:
+        N, T = shape[0], 1
+    elif not packed:
+        if len(shape) != 3:
             raise ValueError("x is [B,T,D]")
-        tok, N, T = tuple(x.shape[:2]), x.shape[0], x.shape[1]
+        N, T = shape[0], shape[1]
     else:
-        if x.dim() not in (2, 3) or (x.dim() == 3 and x.shape[0] != 1):
+        if len(shape) not in (2, 3) or (len(shape) == 3 and shape[0] != 1):
             raise ValueError("packed tensors are [T,D] or [1,T,D]")
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        if len(cu_seqlens[0]) != 1 or cu_seqlens[0][0] < 1:
             raise ValueError("cu_seqlens must be a 1-D tensor of N+1 offsets")
-        _check(cu_seqlens, "cu_seqlens", tuple(cu_seqlens.shape), (torch.int32,), x.device)
-        tok, N, T = tuple(x.shape[:-1]), cu_seqlens.numel() - 1, x.shape[-2]
-    D = x.shape[-1]
+        like(cu_seqlens, "cu_seqlens", cu_seqlens[0], (torch.int32,), dev)
+        N, T = cu_seqlens[0][0] - 1, shape[-2]
+    D = shape[-1]
     if D < 1:
         raise ValueError("x needs at least one channel")
-    code = _dtype_code(x, "x")
-    _like(x, "x", x.shape, x.dtype, x.device)
-    gcode = _dtype_code(log_decay, "log_decay")
-    _like(log_decay, "log_decay", x.shape, log_decay.dtype, x.device)
-    return tok, (N, T, D, code, gcode, int(bool(gate_logits)), int(bool(complement)))
-
-
-def _marks_shape(x, cu_seqlens, T):
+    code, gcode = _type_code(dtype, "x"), _type_code(log_decay[2], "log_decay")
+    like(x, "x", shape, (dtype,), dev)
+    like(log_decay, "log_decay", shape, (log_decay[2],), dev)
+    for name, f in states:
+        if f is not None:
+            like(f, name, (N, D), (torch.float32,), dev)
+    for name, f in tokens:
+        if f is not None:
+            like(f, name, shape, (dtype,), dev)
+    desc = make_scan_desc(N, T, D, code, gcode, int(gate_logits), int(complement))
     n = (T + SCAN_MARK - 1) // SCAN_MARK
-    return (n, x.shape[-1]) if cu_seqlens is not None else (x.shape[0], n, x.shape[-1])
+    need = 0 if kind == "step" else _bytes(f"gdn2_scan_{kind}{'_varlen' if packed else ''}_workspace", desc)
+    return desc, need, N, (n, D) if packed else (shape[0], n, D)
 
 
 def _fwd(x, log_decay, cu_seqlens, state0, gate_logits, complement, out, state_out, return_state, return_marks, workspace):
     import torch
-    tok, sizes = _sizes(x, log_decay, cu_seqlens, gate_logits, complement)
-    N, T, D = sizes[:3]
+    desc, need, N, mshape = _request("fwd", facts(x), facts(log_decay), facts(cu_seqlens), bool(gate_logits), bool(complement),
+                                     (("state0", facts(state0)), ("state_out", facts(state_out))), ("out", facts(out)))
     dev, f32 = x.device, torch.float32
-    if state0 is not None:
-        _like(state0, "state0", (N, D), f32, dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = x.new_empty(x.shape)
+    if state_out is None and return_state:
+        state_out = torch.empty((N, x.shape[-1]), dtype=f32, device=dev)
+    marks = torch.empty(mshape, dtype=f32, device=dev) if return_marks else None
+    ws, n = _space(workspace, need, dev)
+    if cu_seqlens is None:
+        _run("gdn2_scan_fwd", dev, desc, _ptr(x), _ptr(log_decay), _ptr(state0), _ptr(out), _ptr(state_out), _ptr(marks), _ptr(ws), n)
     else:
-        _like(out, "out", x.shape, x.dtype, dev)
-    if state_out is not None:
-        _like(state_out, "state_out", (N, D), f32, dev)
-    elif return_state:
-        state_out = torch.empty((N, D), dtype=f32, device=dev)
-    marks = torch.empty(_marks_shape(x, cu_seqlens, T), dtype=f32, device=dev) if return_marks else None
-    name = "gdn2_scan_fwd" if cu_seqlens is None else "gdn2_scan_fwd_varlen"
-    ws, n = _space(workspace, _need(name + "_workspace", make_scan_desc, *sizes), dev)
-    _run(name, dev, make_scan_desc(*sizes), *([] if cu_seqlens is None else [_ptr(cu_seqlens)]), _ptr(x), _ptr(log_decay), _ptr(state0),
-         _ptr(out), _ptr(state_out), _ptr(marks), _ptr(ws), n)
+        _run("gdn2_scan_fwd_varlen", dev, desc, _ptr(cu_seqlens), _ptr(x), _ptr(log_decay), _ptr(state0), _ptr(out), _ptr(state_out),
+             _ptr(marks), _ptr(ws), n)
     return out, state_out, marks
 
 
@@ -134,22 +143,21 @@ def gated_scan_fwd_varlen(x, log_decay, cu_seqlens, state0=None, gate_logits=Fal
 
 def _bwd(dy, x, log_decay, marks, cu_seqlens, state0, d_state, gate_logits, complement, want_state0, workspace):
     import torch
-    tok, sizes = _sizes(x, log_decay, cu_seqlens, gate_logits, complement)
-    N, T, D = sizes[:3]
+    desc, need, N, mshape = _request("bwd", facts(x), facts(log_decay), facts(cu_seqlens), bool(gate_logits), bool(complement),
+                                     (("state0", facts(state0)), ("d_state", facts(d_state))), ("dy", facts(dy)))
     dev, f32 = x.device, torch.float32
-    _like(dy, "dy", x.shape, x.dtype, dev)
-    _like(marks, "marks", _marks_shape(x, cu_seqlens, T), f32, dev)
-    for t, n in ((state0, "state0"), (d_state, "d_state")):
-        if t is not None:
-            _like(t, n, (N, D), f32, dev)
+    like(facts(marks), "marks", mshape, (f32,), dev)
     if want_state0 is None:
         want_state0 = state0 is not None
-    dx, dg = torch.empty_like(x), torch.empty_like(log_decay)
-    ds0 = torch.empty((N, D), dtype=f32, device=dev) if want_state0 else None
-    name = "gdn2_scan_bwd" if cu_seqlens is None else "gdn2_scan_bwd_varlen"
-    ws, n = _space(workspace, _need(name + "_workspace", make_scan_desc, *sizes), dev)
-    _run(name, dev, make_scan_desc(*sizes), *([] if cu_seqlens is None else [_ptr(cu_seqlens)]), _ptr(dy), _ptr(x), _ptr(log_decay),
-         _ptr(marks), _ptr(state0), _ptr(d_state), _ptr(dx), _ptr(dg), _ptr(ds0), _ptr(ws), n)
+    dx, dg = x.new_empty(x.shape), log_decay.new_empty(x.shape)
+    ds0 = torch.empty((N, x.shape[-1]), dtype=f32, device=dev) if want_state0 else None
+    ws, n = _space(workspace, need, dev)
+    if cu_seqlens is None:
+        _run("gdn2_scan_bwd", dev, desc, _ptr(dy), _ptr(x), _ptr(log_decay), _ptr(marks), _ptr(state0), _ptr(d_state), _ptr(dx), _ptr(dg),
+             _ptr(ds0), _ptr(ws), n)
+    else:
+        _run("gdn2_scan_bwd_varlen", dev, desc, _ptr(cu_seqlens), _ptr(dy), _ptr(x), _ptr(log_decay), _ptr(marks), _ptr(state0),
+             _ptr(d_state), _ptr(dx), _ptr(dg), _ptr(ds0), _ptr(ws), n)
     return dict(dx=dx, d_log_decay=dg, d_state0=ds0)
 
 
@@ -180,12 +188,9 @@ def gated_scan_step(x, log_decay, state, gate_logits=False, complement=False, ou
 
     x, log_decay [N,D] as for ``gated_scan_fwd``.  Returns y like x.
     """
-    import torch
-    tok, sizes = _sizes(x, log_decay, None, gate_logits, complement, step=True)
-    _like(state, "state", x.shape, torch.float32, x.device)
+    desc, _, _, _ = _request("step", facts(x), facts(log_decay), None, bool(gate_logits), bool(complement),
+                             (("state", facts(state)),), ("out", facts(out)))
     if out is None:
-        out = torch.empty_like(x)
-    else:
-        _like(out, "out", x.shape, x.dtype, x.device)
-    _run("gdn2_scan_step", x.device, make_scan_desc(*sizes), _ptr(x), _ptr(log_decay), _ptr(state), _ptr(out))
+        out = x.new_empty(x.shape)
+    _run("gdn2_scan_step", x.device, desc, _ptr(x), _ptr(log_decay), _ptr(state), _ptr(out))
     return out

@@ -5,14 +5,22 @@ Bounds, elementwise, with e = 2^-24 (half a step of fp32, relative).  A cosine
 or sine of the kernel: the reduced angle is at most pi/4 and rounded twice (1.6
 e), the series adds at most 3 e and the magnitude's product 1 e, together below
 6 e m.  A turned element sums two products of it: 2 more roundings of each
-product, so it is off by at most 9 e m (|u| + |v|), T below.  Behind the norm
-two more roundings come (x r and the weight): 11 e.  Backward, a channel sum of
-d terms is added up by lanes of at most 16 terms, then over at most 64 lanes (6
-additions), each rounding its partial sum: 22 e beside the 12 e of its terms;
-with the last products dx is off by at most 48 e r (w T + |h| n sum w T |h|).  A
-weight's gradient is a sum over rows: a lane adds at most 40 in fp32, then come
-at most 8 joins; with 12 e of the terms 64 e sum T |h|.  A bf16 result is
-rounded once more, by at most 2^-8 of it.
+product, so it is off by at most 9 e m (|u| + |v|), T below.
+
+The norm's sum of squares: a lane adds at most 16 squares in four sums (4
+products and 4 sums each) and joins them (2), then come at most 6 joins over
+lanes, the mean's product and eps: 18 e of it, 9 e of r = 1 / sqrt.  The root's
+approximation (2 e) is refined by a step of three products, a difference and a
+product: 3.5 e.  With h = x r that makes 13.5 e of h, 15 e of w h, and 24 e m (|wh|
++ |wh'|) behind the turn.  (Rows summed in 64 bits have less.)
+
+Backward: w g is off by 10 e; a term w g h of the channel sum by 25 e, and the
+sum is added up by lanes of at most 16 terms, then over at most 64 lanes (6
+joins), each rounding its partial sum: 22 e more; h n sum is off by 13.5 + 48 + 2
+e; with the difference and r's product dx is off by at most 80 e r (w T + |h| n
+sum w T |h|).  A weight's gradient is a sum over rows of g h, each off by 24 e: a
+lane adds at most 40 in fp32, then come at most 8 joins: 72 e sum T |h|.  A bf16
+result is rounded once more, by at most 2^-8 of it.
 """
 from __future__ import annotations
 
@@ -68,9 +76,9 @@ def norm_turn(x, w, freq, positions, offset, inter, m, norm, eps):
     y = x * _inverse(x, norm, eps)
     y = y if w is None else y * _d(w)
     if freq is None:
-        return y, 3 * E * y.abs()
+        return y, 15 * E * y.abs()
     y, size = rotate(y, angles(tuple(x.shape[:-2]), freq, positions, offset), m, inter)
-    return y, 11 * E * size
+    return y, 24 * E * size
 
 
 def norm_turn_backward(dy, x, w, freq, positions, offset, inter, m, norm, eps):
@@ -85,9 +93,9 @@ def norm_turn_backward(dy, x, w, freq, positions, offset, inter, m, norm, eps):
         g, size = rotate(dy, angles(tuple(x.shape[:-2]), freq, positions, offset), m, inter, back=True)
     dx = r * (w * g - h * n * (w * g * h).sum(-1, keepdim=True))
     t = w.abs() * size
-    bound = 48 * E * r * (t + h.abs() * n * (t * h.abs()).sum(-1, keepdim=True))
+    bound = 80 * E * r * (t + h.abs() * n * (t * h.abs()).sum(-1, keepdim=True))
     axes = tuple(range(x.dim() - 1))
-    return dx, (g * h).sum(axes), bound, 64 * E * (size * h.abs()).sum(axes)
+    return dx, (g * h).sum(axes), bound, 72 * E * (size * h.abs()).sum(axes)
 
 
 def check(name, got, want, bound):
