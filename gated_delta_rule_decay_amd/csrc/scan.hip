@@ -76,7 +76,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 size_t seq_bytes(const ScanArgs &a) { return a.cu ? align256((static_cast<size_t>(a.T) + 2) * 4) : 0; }
 int64_t words_of(const ScanArgs &a) {
     const int64_t tiles = tiles_of(a);
-    return tiles > 1 ? chains_of(a) * (tiles + tiles / STRIDE) * CW : 0;
+    return tiles > 1 ? chains_of(a) * (tiles + tiles / RUN + tiles / SPAN) * CW : 0;
 }
 
 }  // namespace
@@ -85,13 +85,15 @@ hipError_t prepare(const ScanArgs &a, void *ws, const float *from, float *to, Ch
     char *p = static_cast<char *>(ws);
     ch.tiles = static_cast<int>(tiles_of(a));
     ch.chains = static_cast<int>(chains_of(a));
-    ch.groups = ch.chains < GROUPS ? ch.chains : GROUPS;
+    ch.share = (ch.chains + GROUPS - 1) / GROUPS;
+    ch.groups = (ch.chains + ch.share - 1) / ch.share;
     ch.seq = reinterpret_cast<int *>(p);
     p += seq_bytes(a);
     ch.counters = reinterpret_cast<unsigned *>(p);
     p += align256(COUNTER_WORDS * 4);
     ch.maps = reinterpret_cast<uint64_t *>(p);
-    ch.states = ch.maps + static_cast<int64_t>(ch.chains) * ch.tiles * CW;
+    ch.runs = ch.maps + static_cast<int64_t>(ch.chains) * ch.tiles * CW;
+    ch.states = ch.runs + static_cast<int64_t>(ch.chains) * (ch.tiles / RUN) * CW;
     const int64_t words = words_of(a);
     if (!a.cu && !words) return hipSuccess;
     int64_t work = a.cu ? a.T + 2 : 0;

@@ -11,10 +11,10 @@ template <class T, class G, int VE, int FORM, bool PACKED>
 __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 3) : 4) scan_bwd_kernel(ScanArgs a, Chain ch) {
     using Q = Lanes<VE, NTH>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
-    __shared__ float2 s_map[Q::GRP][CW], s_rev[Q::GRP][CW];
-    __shared__ float2 s_part[PARTS][CW], s_rpart[PARTS][CW], s_look[PARTS][CW];
+    __shared__ float2 s_map[Q::GRP][Q::ROW], s_rev[Q::GRP][Q::ROW];
+    __shared__ float2 s_part[PARTS][CW], s_rpart[PARTS][CW], s_maps[PARTS][CW], s_runs[PARTS][CW];
     __shared__ float s_start[CW];
-    __shared__ int s_tile;
+    __shared__ unsigned s_take;
     const int blocks = static_cast<int>((a.D + CW - 1) / CW), states = PACKED ? static_cast<int>(a.N) : 1;
     const int l = threadIdx.x % Q::LPR, g = threadIdx.x / Q::LPR;
     const int jc = threadIdx.x % CW, jp = __builtin_amdgcn_readfirstlane(threadIdx.x / CW);
@@ -23,11 +23,12 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
     // packed: the states of the sequences
     const auto b0 = buffer<float>(a.s0, 0, PACKED && a.s0 ? states * D : 0), bd = buffer<float>(a.d_sT, 0, PACKED && a.d_sT ? states * D : 0);
 
-    if (threadIdx.x == 0) s_tile = next_tile(ch, true);
+    if (threadIdx.x == 0) s_take = take(ch, true);
     __syncthreads();
-    int tile = __builtin_amdgcn_readfirstlane(s_tile);
+    int tile = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take));
     while (tile >= 0) {
-        const int next = jp == 0 ? take(ch, false) : 0;
+        unsigned next = 0;
+        if (threadIdx.x == 0) next = take(ch, false);
         // steps of a chain go from its last tile to its first
         const Spot p = spot_of<PACKED>(ch, a.T, blocks, tile, true);
         const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
@@ -37,10 +38,10 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
         float V[K][VE];  // decays, see small_of_log
         Rows<K, PACKED> rw;
         // the state that enters the tile, and the gradient that enters the chain
-        float h = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.marks, p.mark * a.D, D), 4 * (p.cb + jc), 0, 0));
-        float r0 = 0.f, r = 0.f;
-        if (!PACKED && p.step == 0 && jp == 0)
-            r0 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.d_sT, p.sequence * a.D, a.d_sT ? D : 0), 4 * (p.cb + jc), 0, 0));
+        float h = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.marks, p.mark * a.D, D), 4 * (p.cb + Q::channel(jc)), 0, 0));
+        float r0 = 0.f;
+        if (!PACKED && p.step == 0)
+            r0 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.d_sT, p.sequence * a.D, a.d_sT ? D : 0), 4 * (p.cb + Q::channel(jc)), 0, 0));
         {
             Row<G, VE> gt[K];
             const auto bx = buffer<T>(a.x, base, p.rows * D), bg = buffer<G>(a.gate, base, p.rows * D), by = buffer<T>(a.dy, base, p.rows * D);
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
                 gt[k].load(bg, at(k, sizeof(G)));
                 dy[k].load(by, at(k, sizeof(T)));
             }
-            rw.read(ch.seq, p.row, g * K, p.rows);
+            rw.load(ch.seq, p.row, g * K, p.rows);
             auto gates = [&](auto f) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
             if (form.logits) gates([](float y) { return small_of_logit(y); });
             else gates([](float y) { return small_of_log(y); });
         }
+        const bool edges = PACKED && rw.edges();
         {
             // maps of the group: forward (fa, fu), backward (ra, ru)
             float fa[VE], fu[VE], ra[VE], ru[VE];
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
                 float h0[VE], d0[VE];
 #pragma unroll
                 for (int e = 0; e < VE; ++e) h0[e] = d0[e] = 0.f;
-                if (PACKED && rw.edges) {
+                if (PACKED && edges) {
                     Row<float, VE> i, o;
                     i.load(b0, rw.state(k, rw.first(k), D, c4));
                     o.load(bd, rw.state(k, rw.last(k), D, c4));
@@ -106,12 +108,12 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
             }
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                s_map[g][l * VE + e] = make_float2(fa[e], fu[e]);
-                s_rev[g][l * VE + e] = make_float2(ra[e], ru[e]);
+                s_map[g][Q::place(l, e)] = make_float2(fa[e], fu[e]);
+                s_rev[g][Q::place(l, e)] = make_float2(ra[e], ru[e]);
             }
         }
         __syncthreads();
-        if (jp == 0) s_tile = __builtin_amdgcn_readfirstlane(next);
+        if (jp == 0) s_take = __builtin_amdgcn_readfirstlane(next);
         {
             float2 m = make_float2(1.f, 0.f), n = make_float2(1.f, 0.f);
 #pragma unroll 4
@@ -124,25 +126,15 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
             s_rpart[jp][jc] = n;
         }
         __syncthreads();
-        tile = __builtin_amdgcn_readfirstlane(s_tile);
+        tile = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take));
+        float r = r0;
         if (ch.tiles > 1) {
-            if (jp == 0 && p.step + 1 < ch.tiles) {
-                float2 n = s_rpart[0][jc];
+            float2 n = s_rpart[0][jc];
 #pragma unroll
-                for (int i = 1; i < PARTS; ++i) n = make_float2(n.x * s_rpart[i][jc].x, n.x * s_rpart[i][jc].y + n.y);
-                if (p.step == 0) n = make_float2(0.f, n.x * r0 + n.y);
-                leave(ch.maps + (p.chain * ch.tiles + p.step) * CW + jc, n.x, n.y);
-            }
-            s_look[jp][jc] = look_back<Q::LOOK>(ch, p.chain, p.step, jc, jp, r0, r);
-            if (jp == 0) s_start[jc] = r;
-            __syncthreads();
-            r = s_start[jc];
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) r = s_look[i][jc].x * r + s_look[i][jc].y;
-        } else {
-            if (jp == 0) s_start[jc] = r0;
-            __syncthreads();
-            r = s_start[jc];
+            for (int i = 1; i < PARTS; ++i) n = make_float2(n.x * s_rpart[i][jc].x, n.x * s_rpart[i][jc].y + n.y);
+            LookBack<Q::LOOK> back;
+            back.start(ch, p.chain, p.step, jc, jp);
+            r = enter<PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, n, r0, s_maps, s_runs, s_start);
         }
         for (int i = 0; i < jp; ++i) h = s_part[i][jc].x * h + s_part[i][jc].y;
         for (int i = PARTS - 1; i > jp; --i) r = s_rpart[i][jc].x * r + s_rpart[i][jc].y;
@@ -160,8 +152,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
             m.y = r;
             r = next_r;
         }
-        if (jp == 0 && p.step % STRIDE == STRIDE - 1 && p.step + 1 < ch.tiles)
-            leave(ch.states + (p.chain * (ch.tiles / STRIDE) + p.step / STRIDE) * CW + jc, 0.f, r);
+        if (jp == 0) leave_state(ch, p.chain, p.step, jc, r);
         __syncthreads();
         // decoded again below: a and w of all tokens would not fit beside the states
 #pragma unroll
@@ -172,12 +163,12 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
         float H[K][VE], rv[VE];  // H: the states that enter the tokens
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-            H[0][e] = s_map[g][l * VE + e].y;
-            rv[e] = s_rev[g][l * VE + e].y;
+            H[0][e] = s_map[g][Q::place(l, e)].y;
+            rv[e] = s_rev[g][Q::place(l, e)].y;
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (PACKED && rw.edges) {
+            if (PACKED && edges) {
                 Row<float, VE> i;
                 i.load(b0, rw.state(k, rw.first(k), D, c4));
 #pragma unroll
@@ -192,12 +183,12 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < VE; ++e) settle(V[k][e]);
-        const bool starts = a.d_s0 != nullptr && (PACKED ? rw.edges : p.step == ch.tiles - 1 && jp == 0);
+        const bool starts = a.d_s0 != nullptr && (PACKED ? edges : p.step == ch.tiles - 1 && jp == 0);
         const auto bs = PACKED ? buffer<float>(a.d_s0, 0, states * D) : buffer<float>(a.d_s0, p.sequence * a.D, D);
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
             float gx[VE], gl[VE];
-            if (PACKED && rw.edges) {
+            if (PACKED && edges) {
                 Row<float, VE> o;
                 o.load(bd, rw.state(k, rw.last(k), D, c4));
 #pragma unroll

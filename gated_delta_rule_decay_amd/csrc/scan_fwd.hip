@@ -8,59 +8,75 @@ namespace {
 constexpr int NTH = 256;  // lanes of a workgroup where each holds 8 channels
 
 template <class T, class G, int VE, int FORM, bool PACKED>
-__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 && (PACKED || sizeof(T) != sizeof(G)) ? 3 : 4) scan_fwd_kernel(ScanArgs a, Chain ch) {
+__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fwd_kernel(ScanArgs a, Chain ch) {
     using Q = Lanes<VE, NTH>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
-    __shared__ float2 s_map[Q::GRP][CW];  // groups' maps, then .y the state that enters
-    __shared__ float2 s_part[PARTS][CW], s_look[PARTS][CW];
+    __shared__ float2 s_map[Q::GRP][Q::ROW];  // groups' maps, then .y the state that enters
+    __shared__ float2 s_part[PARTS][CW], s_maps[PARTS][CW], s_runs[PARTS][CW];
     __shared__ float s_start[CW];
-    __shared__ int s_tile;
+    __shared__ unsigned s_take[2];
     const int blocks = static_cast<int>((a.D + CW - 1) / CW), states = PACKED ? static_cast<int>(a.N) : 1;
     const int l = threadIdx.x % Q::LPR, g = threadIdx.x / Q::LPR;
-    const int jc = threadIdx.x % CW, jp = __builtin_amdgcn_readfirstlane(threadIdx.x / CW);  // channel and part of the joint
+    const int jc = threadIdx.x % CW, jp = __builtin_amdgcn_readfirstlane(threadIdx.x / CW);  // place and part in the joint
     const unsigned D = static_cast<unsigned>(a.D);
     const Form<FORM> form(a);
 
-    if (threadIdx.x == 0) s_tile = next_tile(ch, true);
+    // of a tile, as loaded
+    Row<T, VE> x[K];
+    Row<G, VE> gt[K];
+    Rows<K, PACKED> ahead;
+    auto fetch = [&](const Spot &p) {
+        const unsigned c = p.cb + l * VE, lane = g * K * D + c;
+        const int64_t base = p.row * a.D;
+        const auto bx = buffer<T>(a.x, base, p.rows * D), bg = buffer<G>(a.gate, base, p.rows * D);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k].load(bx, (c < D ? lane * sizeof(T) : NOWHERE) + k * D * sizeof(T));
+            gt[k].load(bg, (c < D ? lane * sizeof(G) : NOWHERE) + k * D * sizeof(G));
+        }
+        ahead.load(ch.seq, p.row, g * K, p.rows);
+    };
+
+    if (threadIdx.x == 0) {
+        s_take[0] = take(ch, true);
+        s_take[1] = take(ch, false);
+    }
     __syncthreads();
-    int tile = __builtin_amdgcn_readfirstlane(s_tile);
+    int tile = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take[0])), after = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take[1]));
+    if (tile < 0) return;
+    Spot p = spot_of<PACKED>(ch, a.T, blocks, tile, false);
+    fetch(p);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): in the loop the loads are waited for over the stores behind them
     while (tile >= 0) {
-        const int next = jp == 0 ? take(ch, false) : 0;
-        const Spot p = spot_of<PACKED>(ch, a.T, blocks, tile, false);
+        unsigned next = 0;
+        if (threadIdx.x == 0) next = take(ch, false);
         const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
         const int64_t base = p.row * a.D;
         auto at = [&](int k, unsigned size) { return (c < D ? lane * size : NOWHERE) + k * D * size; };
         float A[K][VE], U[K][VE];
-        Rows<K, PACKED> rw;
-        {
-            Row<T, VE> x[K];
-            Row<G, VE> gt[K];
-            const auto bx = buffer<T>(a.x, base, p.rows * D), bg = buffer<G>(a.gate, base, p.rows * D);
+        const Rows<K, PACKED> rw = ahead;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                x[k].load(bx, at(k, sizeof(T)));
-                gt[k].load(bg, at(k, sizeof(G)));
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float v = form.logits ? small_of_logit(gt[k][e]) : small_of_log(gt[k][e]);
+                A[k][e] = decay_of(v);
+                U[k][e] = form.comp ? rest_of(v) * x[k][e] : x[k][e];
+                settle(A[k][e]);
+                settle(U[k][e]);
             }
-            rw.read(ch.seq, p.row, g * K, p.rows);
-            auto gates = [&](auto f) {
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        f(gt[k][e], x[k][e], A[k][e], U[k][e]);
-                        settle(A[k][e]);
-                        settle(U[k][e]);
-                    }
-            };
-            gates([&](float y, float x, float &A, float &U) {
-                const float v = form.logits ? small_of_logit(y) : small_of_log(y);
-                A = decay_of(v);
-                U = form.comp ? rest_of(v) * x : x;
-            });
+        const bool edges = PACKED && rw.edges();
+        float h0 = 0.f;
+        if (!PACKED && p.step == 0) {  // what the chain starts from
+            h0 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.s0, p.sequence * a.D, a.s0 ? D : 0),
+                                                                     4 * (p.cb + Q::channel(jc)), 0, 0));
+            settle(h0);  // not waited for elsewhere
         }
+        LookBack<Q::LOOK> back;
+        back.start(ch, p.chain, p.step, jc, jp);
         const bool marked = a.marks != nullptr && jp == 0;  // the tile's first row is in wave 0
         const auto bm = buffer<float>(a.marks, p.mark * a.D, marked ? D : 0);
-        if (PACKED && rw.edges) {  // sequences start: from state0, and from nothing before
+        if (PACKED && edges) {  // sequences start: from state0, and from nothing before
             const auto b0 = buffer<float>(a.s0, 0, a.s0 ? states * D : 0);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -94,13 +110,10 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 && (PACKED || si
                     ca[e] *= A[k][e];
                 }
 #pragma unroll
-            for (int e = 0; e < VE; ++e) s_map[g][l * VE + e] = make_float2(ca[e], cu[e]);
+            for (int e = 0; e < VE; ++e) s_map[g][Q::place(l, e)] = make_float2(ca[e], cu[e]);
         }
-        float h0 = 0.f, h = 0.f;
-        if (!PACKED && p.step == 0 && jp == 0)
-            h0 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.s0, p.sequence * a.D, a.s0 ? D : 0), 4 * (p.cb + jc), 0, 0));
         __syncthreads();
-        if (jp == 0) s_tile = __builtin_amdgcn_readfirstlane(next);
+        if (jp == 0) s_take[0] = __builtin_amdgcn_readfirstlane(next);
         {
             float2 m = make_float2(1.f, 0.f);
 #pragma unroll
@@ -111,26 +124,22 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 && (PACKED || si
             s_part[jp][jc] = m;
         }
         __syncthreads();
-        tile = __builtin_amdgcn_readfirstlane(s_tile);
+        tile = after;
+        after = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take[0]));
+        float h = h0;
         if (ch.tiles > 1) {
-            if (jp == 0 && p.step + 1 < ch.tiles) {
-                float2 m = s_part[0][jc];
+            float2 m = s_part[0][jc];
 #pragma unroll
-                for (int i = 1; i < PARTS; ++i) m = make_float2(s_part[i][jc].x * m.x, s_part[i][jc].x * m.y + s_part[i][jc].y);
-                if (p.step == 0) m = make_float2(0.f, m.x * h0 + m.y);  // the later tiles do not read state0
-                leave(ch.maps + (p.chain * ch.tiles + p.step) * CW + jc, m.x, m.y);
-            }
-            s_look[jp][jc] = look_back<Q::LOOK>(ch, p.chain, p.step, jc, jp, h0, h);
-            if (jp == 0) s_start[jc] = h;
-            __syncthreads();
-            h = s_start[jc];
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) h = s_look[i][jc].x * h + s_look[i][jc].y;
-        } else {
-            if (jp == 0) s_start[jc] = h0;
-            __syncthreads();
-            h = s_start[jc];
+            for (int i = 1; i < PARTS; ++i) m = make_float2(s_part[i][jc].x * m.x, s_part[i][jc].x * m.y + s_part[i][jc].y);
+            h = enter<PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, m, h0, s_maps, s_runs, s_start);
         }
+        // The next tile's loads are in flight from here to the next round; behind
+        // the last tile they read zeros.  (From before the wait for the words,
+        // where a second look waits for them as well: 311 us for 65536 tokens of
+        // 2048 channels, from here 296.)
+        Spot q = spot_of<PACKED>(ch, a.T, blocks, tile < 0 ? 0 : tile, false);
+        if (tile < 0) q.rows = 0;
+        fetch(q);
         for (int i = 0; i < jp; ++i) h = s_part[i][jc].x * h + s_part[i][jc].y;
 #pragma unroll
         for (int i = 0; i < Q::PER; ++i) {
@@ -139,16 +148,15 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 && (PACKED || si
             m.y = h;
             h = next_h;
         }
-        if (jp == PARTS - 1 && p.step % STRIDE == STRIDE - 1 && p.step + 1 < ch.tiles)
-            leave(ch.states + (p.chain * (ch.tiles / STRIDE) + p.step / STRIDE) * CW + jc, 0.f, h);
+        if (jp == PARTS - 1) leave_state(ch, p.chain, p.step, jc, h);
         __syncthreads();
         const auto by = buffer<T>(a.y, base, p.rows * D);
         float hv[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) hv[e] = s_map[g][l * VE + e].y;
+        for (int e = 0; e < VE; ++e) hv[e] = s_map[g][Q::place(l, e)].y;
         if (marked) store_row<float, VE>(bm, g == 0 && rw.live(0) && !rw.first(0) ? c4 : NOWHERE, hv);
         // the state behind the last token, in the wave that holds it; packed: behind each sequence's last
-        const bool ends = a.s_out != nullptr && (PACKED ? rw.edges : p.step == ch.tiles - 1);
+        const bool ends = a.s_out != nullptr && (PACKED ? edges : p.step == ch.tiles - 1);
         const auto bs = PACKED ? buffer<float>(a.s_out, 0, states * D) : buffer<float>(a.s_out, p.sequence * a.D, D);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -157,6 +165,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 && (PACKED || si
             store_row<T, VE>(by, rw.live(k) ? at(k, sizeof(T)) : NOWHERE, hv);
             if (ends) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.last(k), D, c4) : g * K + k == p.rows - 1 ? c4 : NOWHERE, hv);
         }
+        p = q;
     }
 }
 
@@ -165,8 +174,9 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 && (PACKED || si
 
 using namespace scan;
 
-// workgroups that run at once
-constexpr int AT_ONCE = 1024;
+// workgroups that run at once (65536 tokens of 2048 channels: 296 us, with 512 of
+// them 310)
+constexpr int AT_ONCE = 768;
 
 hipError_t launch_scan_fwd(const ScanArgs &a, void *ws, hipStream_t s) {
     Chain ch = {};

@@ -14,14 +14,16 @@
 // element is read once.
 //
 // Between tiles (a chain: the tiles of one block of channels of one sequence):
-// a tile leaves its map, and every 16th tile the state behind it, as one 64-bit
-// word a channel, both halves and the fact that it is there in one store.  A
-// tile composes the up to 15 maps since the last such state, always the same
-// ones in the same order, so that results do not depend on the timing.  A
-// workgroup takes its tiles from a counter, tokens ascending, and a tile waits
-// only for tiles that the counter gave out before it, so for workgroups that
-// already run: the wait ends.  (It is bounded all the same, for calls that
-// share a workspace at the same time, which is not allowed.)
+// a tile leaves its map as one 64-bit word a channel, both halves and the fact
+// that it is there in one store; every 16th tile leaves the map of its run of 16
+// as well, and every 256th the state behind it.  A tile composes the state, the
+// up to 15 runs and the up to 15 maps since then, always the same ones in the
+// same order, so that results do not depend on the timing; neither a map nor a
+// run waits for a state, so a chain moves on at the tiles' own pace.  A workgroup takes its tiles from a
+// counter, tokens ascending, and a tile waits only for tiles that the counter
+// gave out before it, so for workgroups that already run: the wait ends.  (It is
+// bounded all the same, for calls that share a workspace at the same time, which
+// is not allowed.)
 //
 // Packed sequences are one axis with resets: at a sequence's first token the
 // state comes from state0, (0, a s0 + u), and backward the gradient that enters
@@ -41,8 +43,9 @@ namespace scan {
 constexpr int CW = 64;  // channels of a workgroup: a wave's lanes in the joint
 constexpr int ROWS = SCAN_MARK;
 static_assert(ROWS == 128, "tiles are marks");
-constexpr int STRIDE = 16;  // tiles from state to state
-constexpr int GROUPS = 8;   // counters, each for every 8th chain: one for all would serialise the workgroups' starts
+constexpr int RUN = 16;         // tiles of a run
+constexpr int SPAN = RUN * 16;  // tiles from state to state
+constexpr int GROUPS = 32;      // counters, each for neighbouring chains: one for all would serialise the workgroups' starts
 constexpr uint64_t NOT_YET = ~uint64_t(0);
 
 // What the workgroups of a launch share, in the workspace.
@@ -50,8 +53,9 @@ struct Chain {
     int *seq;            // packed: [T + 2], 1 + the sequence index of token t at t + 1, 0 outside
     unsigned *counters;  // [GROUPS] at 64-byte steps, then the word that ends all waits
     uint64_t *maps;      // [chains][tiles][CW]
-    uint64_t *states;    // [chains][tiles / STRIDE][CW]
-    int tiles, chains, groups;
+    uint64_t *runs;      // [chains][tiles / RUN][CW]
+    uint64_t *states;    // [chains][tiles / SPAN][CW]
+    int tiles, chains, groups, share;  // share: chains of a group, at most
 };
 constexpr int COUNTER_STEP = 16, COUNTER_WORDS = COUNTER_STEP * (GROUPS + 1);
 
@@ -62,7 +66,7 @@ hipError_t prepare(const ScanArgs &a, void *ws, const float *from, float *to, Ch
 // Workgroups: one a tile where chains are one tile long, else as many as run
 // at once; those that start late find nothing left.
 inline int grid_of(const Chain &ch, int at_once) {
-    const int64_t per = (ch.chains + ch.groups - 1) / ch.groups * static_cast<int64_t>(ch.tiles);  // of a group, at most
+    const int64_t per = static_cast<int64_t>(ch.share) * ch.tiles;  // of a group, at most
     const int64_t most = ch.tiles > 1 ? at_once / ch.groups : per;
     return static_cast<int>((per < most ? per : most) * ch.groups);
 }
@@ -102,7 +106,13 @@ struct Lanes {
     static constexpr int K = ROWS / GRP;         // rows of a group
     static constexpr int PARTS = NTH / CW;       // waves; each composes
     static constexpr int PER = GRP / PARTS;      // groups, and looks back at
-    static constexpr int LOOK = STRIDE / PARTS;  // tiles
+    static constexpr int LOOK = RUN / PARTS;     // tiles and at runs
+    // Where channel l * VE + e of a block stands in the joint, and the channel
+    // that stands at q: neighbouring lanes of a group write to neighbouring
+    // places, and a row of places (ROW) is so long that groups fall on other banks.
+    static constexpr int ROW = CW + (VE > 1 ? 8 : 0);
+    static __device__ __forceinline__ int place(int l, int e) { return e * LPR + l; }
+    static __device__ __forceinline__ int channel(int q) { return q % LPR * VE + q / LPR; }
 };
 
 // The form, compiled in or from the request.
@@ -139,16 +149,33 @@ __device__ __forceinline__ float small_of_logit(float g) {
     return copysignf(e * __builtin_amdgcn_rcpf(1.f + e), g);
 }
 
-// The next tile of a workgroup, in the order in which its counter gives them
-// out, or -1 behind the last.
-__device__ __forceinline__ int next_tile(const Chain &ch, bool start) {
-    const int group = blockIdx.x % ch.groups;
-    const int mine = (ch.chains - group + ch.groups - 1) / ch.groups;  // chains of the group
-    unsigned i;
-    if (ch.tiles > 1) i = __hip_atomic_fetch_add(ch.counters + group * COUNTER_STEP, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    else i = start ? blockIdx.x / ch.groups : INT32_MAX;
-    const unsigned step = i / mine;
-    return step < static_cast<unsigned>(ch.tiles) ? step * ch.chains + group + ch.groups * (i - step * mine) : -1;
+// The counter of a workgroup.  Every 256th runs on the same CU: it gets another
+// chain, because tiles of one chain on one CU take their turns at its issue slots
+// while the others of the chain wait for them (65536 tokens of 2048 channels:
+// 280 us, without the shift 296).  The first 256 reach all counters.
+__device__ __forceinline__ unsigned group_of(const Chain &ch) {
+    return (blockIdx.x + (ch.tiles > 1 ? blockIdx.x / 256 * 11 : 0)) % ch.groups;
+}
+// A workgroup's next number from its counter (without counters: its own, once),
+// and the tile that it stands for, -1 behind the last.
+// (of one lane)
+__device__ __forceinline__ unsigned take(const Chain &ch, bool start) {
+    if (ch.tiles == 1) return start ? blockIdx.x / ch.groups : INT32_MAX;
+    // an address that looks like the lane's own: at a common one the compiler
+    // adds for the whole wave, and waits for the result on the spot
+    unsigned zero = 0;
+    asm volatile("" : "+v"(zero));
+    return __hip_atomic_fetch_add(ch.counters + group_of(ch) * COUNTER_STEP + zero, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ int tile_of(const Chain &ch, unsigned i) {
+    // a group's chains neighbour each other: they share lines of their rows
+    // (65536 rows of 4 KB copied in tiles: 5.45 TB/s, with every 8th block of
+    // channels 4.95)
+    const unsigned first = group_of(ch) * ch.share, left = ch.chains - first;
+    const unsigned mine = left < static_cast<unsigned>(ch.share) ? left : ch.share, step = i / mine;
+    // (the division leaves scalar registers)
+    return __builtin_amdgcn_readfirstlane(
+        step < static_cast<unsigned>(ch.tiles) ? static_cast<int>(step * ch.chains + first + i - step * mine) : -1);
 }
 
 // A channel's word: (factor, addend) of a map, or (anything, state).
@@ -161,55 +188,122 @@ __device__ __forceinline__ float2 word(uint64_t w) {
     return make_float2(__uint_as_float(static_cast<unsigned>(w)), __uint_as_float(static_cast<unsigned>(w >> 32)));
 }
 
-// N words, waited for together by all lanes of a wave; those not wanted read as
-// (1, 0).
-template <int N>
-__device__ __forceinline__ void await(const Chain &ch, const uint64_t *const (&p)[N], const bool (&want)[N], float2 (&v)[N]) {
-    uint64_t w[N];
-    unsigned *end = ch.counters + GROUPS * COUNTER_STEP;
-    for (int spin = 0;; ++spin) {
-        bool there = true;
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = __hip_atomic_load(p[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-        for (int i = 0; i < N; ++i) there = there && (!want[i] || w[i] != NOT_YET);
-        if (__builtin_amdgcn_ballot_w64(!there) == 0) break;
-        // over a hundred times what a launch takes: the workspace is not this call's alone
-        if (spin > (1 << 18)) __hip_atomic_store(end, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if ((spin & 255) == 255 &&
-            __builtin_amdgcn_readfirstlane(__hip_atomic_load(end, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)))
-            break;
-        __builtin_amdgcn_s_sleep(1);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = want[i] ? word(w[i]) : make_float2(1.f, 0.f);
-}
-
-// The map of the tiles of `chain` between the last state and step `i` of it
-// (lane: channel jc, part jp of them), and for part 0 that state itself, or
-// `start` before there is one.  (The first tile's map holds the state that the
-// chain starts from, and no factor: state_out may be state0, and what a later
-// tile stores there comes after the first one's read.)
+// A look at up to 16 words of a chain, first ones of an order (lane: place jc,
+// part jp of the words).  All but `w` is the same in all lanes of a wave.
 template <int LOOK>
-__device__ __forceinline__ float2 look_back(const Chain &ch, int64_t chain, int i, int jc, int jp, float start, float &h) {
-    const int n = i % STRIDE, base = i - n;
-    const uint64_t *maps = ch.maps + (chain * ch.tiles + base) * CW, *states = ch.states + (chain * (ch.tiles / STRIDE) + base / STRIDE - 1) * CW;
-    const uint64_t *p[LOOK + 1];
-    bool want[LOOK + 1];
-    float2 v[LOOK + 1];
+struct Look {
+    const uint64_t *words;
+    int n, first;  // words wanted, the lane's first
+    uint64_t w[LOOK];
+    __device__ __forceinline__ bool want(int k) const { return first + k < n; }
+    // A first look, long before the words are needed.  No branch around its
+    // loads, so that the loads behind them need not be waited for with them:
+    // where there are no words it reads zeros.
+    __device__ __forceinline__ void start(const uint64_t *from, int count, int jc, int jp) {
+        words = from;
+        n = count;
+        first = jp * LOOK;
+        const auto b = buffer<uint64_t>(from, 0, n > 0 ? n * CW : 0);
 #pragma unroll
-    for (int k = 0; k < LOOK; ++k) {
-        want[k] = jp * LOOK + k < n;
-        p[k] = maps + ((want[k] ? jp * LOOK + k : 0) * CW + jc);
+        for (int k = 0; k < LOOK; ++k) {
+            constexpr int SC1 = 16;  // past the caches that other workgroups' stores do not reach
+            w[k] = __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(b, ((want(k) ? first + k : 0) * CW + jc) * 8, 0, SC1));
+        }
     }
-    want[LOOK] = jp == 0 && base > 0;
-    p[LOOK] = want[LOOK] ? states + jc : maps + jc;
-    await<LOOK + 1>(ch, p, want, v);
-    h = base > 0 ? v[LOOK].y : start;
-    float2 m = make_float2(1.f, 0.f);
+    __device__ __forceinline__ void again(int jc) {
+        const unsigned at = jc;
 #pragma unroll
-    for (int k = 0; k < LOOK; ++k) m = make_float2(v[k].x * m.x, v[k].x * m.y + v[k].y);
-    return m;
+        for (int k = 0; k < LOOK; ++k)
+            if (want(k)) w[k] = __hip_atomic_load(words + (first + k) * CW + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ bool there() const {
+        int missing = 0;
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) missing |= want(k) & (w[k] == NOT_YET);
+        return __builtin_amdgcn_ballot_w64(missing != 0) == 0;
+    }
+    // Waits for the words.  (The first look apart from the loop, which waits for
+    // all loads of the wave.)
+    __device__ __forceinline__ void wait(const Chain &ch, int jc) {
+        if (there()) return;
+        unsigned *end = ch.counters + GROUPS * COUNTER_STEP;
+        for (int spin = 0; spin < (1 << 18); ++spin) {
+            __builtin_amdgcn_s_sleep(1);
+            again(jc);
+            if (there()) break;
+            if ((spin & 255) == 255 &&
+                __builtin_amdgcn_readfirstlane(__hip_atomic_load(end, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)))
+                break;
+            // over a hundred times what a launch takes: the workspace is not this call's alone
+            if (spin == (1 << 18) - 1) __hip_atomic_store(end, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    // the words' map
+    __device__ __forceinline__ float2 map() const {
+        float2 m = make_float2(1.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) {
+            const float2 v = want(k) ? word(w[k]) : make_float2(1.f, 0.f);
+            m = make_float2(v.x * m.x, v.x * m.y + v.y);
+        }
+        return m;
+    }
+};
+
+// What tile `step` of a chain looks back at: the maps of its run, the runs of
+// its span, and the state before it (of part 0).  The first tile's map holds the
+// state that the chain starts from, and no factor: state_out may be state0, and
+// what a later tile stores there comes after the first one's read.
+template <int LOOK>
+struct LookBack {
+    Look<LOOK> maps, runs;
+    Look<1> state;
+    __device__ __forceinline__ void start(const Chain &ch, int64_t chain, int step, int jc, int jp) {
+        maps.start(ch.maps + (chain * ch.tiles + step / RUN * RUN) * CW, step % RUN, jc, jp);
+        runs.start(ch.runs + (chain * (ch.tiles / RUN) + step / SPAN * (SPAN / RUN)) * CW, step % SPAN / RUN, jc, jp);
+        state.start(ch.states + (chain * (ch.tiles / SPAN) + step / SPAN - 1) * CW, jp == 0 && step >= SPAN, jc, 0);
+    }
+};
+
+// The state that enters tile `step` of a chain (place jc), for all waves; `own`:
+// the tile's map, `start`: what the chain starts from, both of wave 0 (jp = 0).
+// Leaves the map of a run behind its last tile.  Barriers within.
+template <int PARTS, int LOOK>
+__device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, int64_t chain, int step, int jc, int jp, float2 own,
+                                       float start, float2 (&s_maps)[PARTS][CW], float2 (&s_runs)[PARTS][CW], float (&s_start)[CW]) {
+    if (jp == 0 && step + 1 < ch.tiles) {
+        if (step == 0) own = make_float2(0.f, own.x * start + own.y);
+        leave(ch.maps + (chain * ch.tiles + step) * CW + jc, own.x, own.y);
+    }
+    back.maps.wait(ch, jc);
+    s_maps[jp][jc] = back.maps.map();
+    if (jp == 0) s_start[jc] = start;
+    __syncthreads();
+    if (step >= RUN || step + 1 == RUN) {
+        if (jp == 0 && step % RUN == RUN - 1 && step + 1 < ch.tiles) {
+            float2 m = s_maps[0][jc];
+#pragma unroll
+            for (int i = 1; i < PARTS; ++i) m = make_float2(s_maps[i][jc].x * m.x, s_maps[i][jc].x * m.y + s_maps[i][jc].y);
+            leave(ch.runs + (chain * (ch.tiles / RUN) + step / RUN) * CW + jc, own.x * m.x, own.x * m.y + own.y);
+        }
+        back.runs.wait(ch, jc);
+        s_runs[jp][jc] = back.runs.map();
+        if (jp == 0 && step >= SPAN) {
+            back.state.wait(ch, jc);
+            s_start[jc] = word(back.state.w[0]).y;
+        }
+        __syncthreads();
+    }
+    float h = s_start[jc];
+    if (step >= RUN)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) h = s_runs[i][jc].x * h + s_runs[i][jc].y;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) h = s_maps[i][jc].x * h + s_maps[i][jc].y;
+    return h;
+}
+__device__ __forceinline__ void leave_state(const Chain &ch, int64_t chain, int step, int jc, float h) {
+    if (step % SPAN == SPAN - 1 && step + 1 < ch.tiles) leave(ch.states + (chain * (ch.tiles / SPAN) + step / SPAN) * CW + jc, 0.f, h);
 }
 
 // No lane of the kernels branches by itself while a tile is in registers: what
@@ -286,21 +380,22 @@ __device__ __forceinline__ Spot spot_of(const Chain &ch, int64_t T, int blocks, 
 template <int K, bool PACKED>
 struct Rows {
     int sq[K + 2];
-    bool edges;  // in any lane of the wave
-    __device__ __forceinline__ void read(const int *seq, int64_t row, int r0, int rows) {
+    __device__ __forceinline__ void load(const int *seq, int64_t row, int r0, int rows) {
         if constexpr (PACKED) {
             const auto b = buffer<int>(seq, row, rows + 2);
 #pragma unroll
             for (int k = 0; k < K + 2; ++k) sq[k] = __builtin_amdgcn_raw_buffer_load_b32(b, (r0 + k) * 4, 0, 0);
-            bool edge = false;
-#pragma unroll
-            for (int k = 0; k < K; ++k) edge = edge || first(k) || last(k);
-            edges = __builtin_amdgcn_ballot_w64(edge) != 0;
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k) sq[k + 1] = r0 + k < rows;
-            edges = false;
         }
+    }
+    // whether some lane of the wave has a sequence's first or last token
+    __device__ __forceinline__ bool edges() const {
+        bool edge = false;
+#pragma unroll
+        for (int k = 0; k < K; ++k) edge = edge || first(k) || last(k);
+        return __builtin_amdgcn_ballot_w64(edge) != 0;
     }
     __device__ __forceinline__ bool live(int k) const { return sq[k + 1] != 0; }
     __device__ __forceinline__ bool first(int k) const { return PACKED && live(k) && sq[k] != sq[k + 1]; }
@@ -310,13 +405,6 @@ struct Rows {
         return on ? static_cast<unsigned>(sq[k + 1] - 1) * (D * 4) + c4 : NOWHERE;
     }
 };
-
-// The next tile's number, for all lanes of wave 0; other waves get nothing.
-__device__ __forceinline__ int take(const Chain &ch, bool start) {
-    int t = 0;
-    if (threadIdx.x == 0) t = next_tile(ch, start);
-    return t;
-}
 
 }  // namespace
 }  // namespace scan

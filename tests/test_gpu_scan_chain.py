@@ -15,7 +15,7 @@ def g():
     return pkg
 
 
-# 1 to 3 tiles, the 15th to 17th (a state is left behind the 16th), and the 33rd
+# 1 to 3 tiles, the 15th to 17th (the map of a run is left behind the 16th), and the 33rd
 @pytest.mark.parametrize("tiles", [2, 3, 15, 16, 17, 32, 33, 50])
 @pytest.mark.parametrize("D", [64, 72, 3])
 def test_tiles(g, tiles, D):
@@ -26,7 +26,26 @@ def test_tiles(g, tiles, D):
         check_backward(d, r, False, False)
 
 
-@pytest.mark.parametrize("N,D", [(1, 1), (7, 64), (9, 64), (3, 200), (20, 130)])
+# a state is left behind every 256th tile
+@pytest.mark.parametrize("tiles,D", [(256, 8), (257, 3), (258, 8), (273, 8), (513, 8)])
+def test_tiles_behind_a_state(g, tiles, D):
+    d = make(1, 128 * tiles - tiles % 3, D, BF, seed=tiles)
+    y, S, marks, r = both(g, d, False, True)
+    check_forward(d, y, S, marks, False, True)
+    check_backward(d, r, False, True)
+
+
+def test_sequences_over_a_state(g):
+    # packed: the axis is one chain, sequences end on both sides of its 256th tile
+    lens = [32767, 1, 700, 33500]
+    d = make(len(lens), sum(lens), 8, F32, packed=True, seed=8)
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).int().cuda()
+    y, S, marks, r = both(g, d, True, True, cu)
+    check_forward(d, y, S, marks, True, True, lens)
+    check_backward(d, r, True, True, lens)
+
+
+@pytest.mark.parametrize("N,D", [(1, 1), (7, 64), (9, 64), (3, 200), (20, 130), (33, 64), (11, 230)])
 def test_chains(g, N, D):
     # fewer chains than counters, and numbers that leave them unequal shares
     d = make(N, 2500, D, BF, BF, True, seed=N)
