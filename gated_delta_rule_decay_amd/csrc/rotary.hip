@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
                         }
                         for (int o = L >> 1; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
                         sum = a.l2 ? sum : sum / d + a.eps;
-                        wide = sum > 0.0 ? 1.0 / sqrt(sum) : 0.0;
+                        wide = sum == 0.0 ? 0.0 : 1.0 / sqrt(sum);  // NaN stays
 #pragma unroll
                         for (int e = 0; e < VE; ++e) {
                             u[e] = far ? static_cast<float>(u[e] * wide) : u[e] * rs;

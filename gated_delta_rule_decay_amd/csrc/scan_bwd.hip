@@ -98,12 +98,13 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
                     }
                     u = rw.live(k) ? u : 0.f;
                     y = rw.live(k) ? y : 0.f;
-                    const float in = rw.first(k) ? 0.f : f;
-                    fu[e] = in * fu[e] + u;
-                    fa[e] *= in;
+                    const float h = f * fu[e] + u;
+                    fu[e] = rw.first(k) ? u : h;
+                    fa[e] = rw.first(k) ? RESET : fa[e] * f;
                     // from right to left: the tokens so far come after this one's r
-                    ru[e] += ra[e] * (f * y);
-                    ra[e] = rw.last(k) ? 0.f : ra[e] * f;
+                    const float2 n = joined<PACKED>(make_float2(ra[e], ru[e]), make_float2(rw.last(k) ? RESET : f, f * y));
+                    ra[e] = n.x;
+                    ru[e] = n.y;
                 }
             }
 #pragma unroll
@@ -119,8 +120,8 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
 #pragma unroll 4
             for (int i = 0; i < Q::PER; ++i) {
                 const float2 f = s_map[jp * Q::PER + i][jc], b = s_rev[jp * Q::PER + i][jc];
-                m = make_float2(f.x * m.x, f.x * m.y + f.y);
-                n = make_float2(n.x * b.x, n.x * b.y + n.y);
+                m = joined<PACKED>(f, m);
+                n = joined<PACKED>(n, b);
             }
             s_part[jp][jc] = m;
             s_rpart[jp][jc] = n;
@@ -131,24 +132,24 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
         if (ch.tiles > 1) {
             float2 n = s_rpart[0][jc];
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) n = make_float2(n.x * s_rpart[i][jc].x, n.x * s_rpart[i][jc].y + n.y);
+            for (int i = 1; i < PARTS; ++i) n = joined<PACKED>(n, s_rpart[i][jc]);
             LookBack<Q::LOOK> back;
             back.start(ch, p.chain, p.step, jc, jp);
-            r = enter<PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, n, r0, s_maps, s_runs, s_start);
+            r = enter<PACKED, PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, n, r0, s_maps, s_runs, s_start);
         }
-        for (int i = 0; i < jp; ++i) h = s_part[i][jc].x * h + s_part[i][jc].y;
-        for (int i = PARTS - 1; i > jp; --i) r = s_rpart[i][jc].x * r + s_rpart[i][jc].y;
+        for (int i = 0; i < jp; ++i) h = pass<PACKED>(s_part[i][jc], h);
+        for (int i = PARTS - 1; i > jp; --i) r = pass<PACKED>(s_rpart[i][jc], r);
 #pragma unroll
         for (int i = 0; i < Q::PER; ++i) {
             float2 &m = s_map[jp * Q::PER + i][jc];
-            const float next_h = m.x * h + m.y;
+            const float next_h = pass<PACKED>(m, h);
             m.y = h;
             h = next_h;
         }
 #pragma unroll
         for (int i = Q::PER - 1; i >= 0; --i) {
             float2 &m = s_rev[jp * Q::PER + i][jc];
-            const float next_r = m.x * r + m.y;
+            const float next_r = pass<PACKED>(m, r);
             m.y = r;
             r = next_r;
         }

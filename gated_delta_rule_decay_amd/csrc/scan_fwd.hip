@@ -7,8 +7,15 @@ namespace {
 
 constexpr int NTH = 256;  // lanes of a workgroup where each holds 8 channels
 
+// Workgroups of a CU.  Three, where their registers hold the next tile as well;
+// packed tiles of 6 or 8 bytes an element would spill (7 sequences, 32768 tokens
+// of 2048 channels: bf16 with fp32 gates 163 us with two, 213 with three; fp32
+// 202 and 294; bf16 alone 154 and 150).
+template <class T, class G, bool PACKED>
+constexpr int per_cu() { return PACKED && sizeof(T) + sizeof(G) > 4 ? 2 : 3; }
+
 template <class T, class G, int VE, int FORM, bool PACKED>
-__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fwd_kernel(ScanArgs a, Chain ch) {
+__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), (VE > 1 ? per_cu<T, G, PACKED>() : 4)) scan_fwd_kernel(ScanArgs a, Chain ch) {
     using Q = Lanes<VE, NTH>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
     __shared__ float2 s_map[Q::GRP][Q::ROW];  // groups' maps, then .y the state that enters
@@ -87,7 +94,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fw
                 for (int e = 0; e < VE; ++e) {
                     m[e] = h0[e];
                     U[k][e] += A[k][e] * m[e];
-                    if (rw.first(k)) A[k][e] = 0.f;
+                    A[k][e] = rw.first(k) ? RESET : A[k][e];
                 }
                 // here, not below: another wave may end this sequence, and state_out may be state0
                 if (k == 0) store_row<float, VE>(bm, g == 0 && rw.first(0) ? c4 : NOWHERE, m);
@@ -106,8 +113,9 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fw
                 for (int e = 0; e < VE; ++e) {
                     A[k][e] = rw.live(k) ? A[k][e] : 1.f;
                     U[k][e] = rw.live(k) ? U[k][e] : 0.f;
-                    cu[e] = A[k][e] * cu[e] + U[k][e];
-                    ca[e] *= A[k][e];
+                    const float u = A[k][e] * cu[e] + U[k][e];
+                    cu[e] = rw.first(k) ? U[k][e] : u;
+                    ca[e] = rw.first(k) ? RESET : ca[e] * A[k][e];
                 }
 #pragma unroll
             for (int e = 0; e < VE; ++e) s_map[g][Q::place(l, e)] = make_float2(ca[e], cu[e]);
@@ -117,10 +125,7 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fw
         {
             float2 m = make_float2(1.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < Q::PER; ++i) {
-                const float2 n = s_map[jp * Q::PER + i][jc];
-                m = make_float2(n.x * m.x, n.x * m.y + n.y);
-            }
+            for (int i = 0; i < Q::PER; ++i) m = joined<PACKED>(s_map[jp * Q::PER + i][jc], m);
             s_part[jp][jc] = m;
         }
         __syncthreads();
@@ -130,8 +135,8 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fw
         if (ch.tiles > 1) {
             float2 m = s_part[0][jc];
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) m = make_float2(s_part[i][jc].x * m.x, s_part[i][jc].x * m.y + s_part[i][jc].y);
-            h = enter<PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, m, h0, s_maps, s_runs, s_start);
+            for (int i = 1; i < PARTS; ++i) m = joined<PACKED>(s_part[i][jc], m);
+            h = enter<PACKED, PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, m, h0, s_maps, s_runs, s_start);
         }
         // The next tile's loads are in flight from here to the next round; behind
         // the last tile they read zeros.  (From before the wait for the words,
@@ -140,11 +145,11 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fw
         Spot q = spot_of<PACKED>(ch, a.T, blocks, tile < 0 ? 0 : tile, false);
         if (tile < 0) q.rows = 0;
         fetch(q);
-        for (int i = 0; i < jp; ++i) h = s_part[i][jc].x * h + s_part[i][jc].y;
+        for (int i = 0; i < jp; ++i) h = pass<PACKED>(s_part[i][jc], h);
 #pragma unroll
         for (int i = 0; i < Q::PER; ++i) {
             float2 &m = s_map[jp * Q::PER + i][jc];
-            const float next_h = m.x * h + m.y;
+            const float next_h = pass<PACKED>(m, h);
             m.y = h;
             h = next_h;
         }
@@ -161,7 +166,10 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? 3 : 4) scan_fw
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) hv[e] = A[k][e] * hv[e] + U[k][e];
+            for (int e = 0; e < VE; ++e) {
+                const float h = A[k][e] * hv[e] + U[k][e];
+                hv[e] = rw.first(k) ? U[k][e] : h;
+            }
             store_row<T, VE>(by, rw.live(k) ? at(k, sizeof(T)) : NOWHERE, hv);
             if (ends) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.last(k), D, c4) : g * K + k == p.rows - 1 ? c4 : NOWHERE, hv);
         }

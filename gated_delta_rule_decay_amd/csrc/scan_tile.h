@@ -26,9 +26,11 @@
 // is not allowed.)
 //
 // Packed sequences are one axis with resets: at a sequence's first token the
-// state comes from state0, (0, a s0 + u), and backward the gradient that enters
-// a sequence's last token from behind is d_state_out's.  What a token is comes
-// from a table of sequence indices, one a token, built on the device.
+// state comes from state0, (-0, a s0 + u), and backward the gradient that enters
+// a sequence's last token from behind is d_state_out's.  A factor of -0, which no
+// decay has, takes nothing of what is before it, be it infinite, NaN or the mark
+// of a row of no sequence.  What a token is comes from a table of sequence
+// indices, one a token, built on the device.
 #pragma once
 
 #include <type_traits>
@@ -178,6 +180,20 @@ __device__ __forceinline__ int tile_of(const Chain &ch, unsigned i) {
         step < static_cast<unsigned>(ch.tiles) ? static_cast<int>(step * ch.chains + first + i - step * mine) : -1);
 }
 
+// Maps (factor, addend): `n` after `m`, and of a state.
+constexpr float RESET = -0.f;
+__device__ __forceinline__ bool resets(float factor) { return __float_as_uint(factor) == 0x80000000u; }
+template <bool PACKED>
+__device__ __forceinline__ float pass(float2 n, float h) {
+    const float through = n.x * h + n.y;
+    return PACKED && resets(n.x) ? n.y : through;
+}
+template <bool PACKED>
+__device__ __forceinline__ float2 joined(float2 n, float2 m) {
+    const float u = pass<PACKED>(n, m.y), a = n.x * m.x;
+    return make_float2(PACKED && resets(n.x) ? RESET : a, u);
+}
+
 // A channel's word: (factor, addend) of a map, or (anything, state).
 __device__ __forceinline__ void leave(uint64_t *p, float a, float u) {
     unsigned hi = __float_as_uint(u);
@@ -239,13 +255,11 @@ struct Look {
         }
     }
     // the words' map
+    template <bool PACKED>
     __device__ __forceinline__ float2 map() const {
         float2 m = make_float2(1.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < LOOK; ++k) {
-            const float2 v = want(k) ? word(w[k]) : make_float2(1.f, 0.f);
-            m = make_float2(v.x * m.x, v.x * m.y + v.y);
-        }
+        for (int k = 0; k < LOOK; ++k) m = joined<PACKED>(want(k) ? word(w[k]) : make_float2(1.f, 0.f), m);
         return m;
     }
 };
@@ -268,26 +282,27 @@ struct LookBack {
 // The state that enters tile `step` of a chain (place jc), for all waves; `own`:
 // the tile's map, `start`: what the chain starts from, both of wave 0 (jp = 0).
 // Leaves the map of a run behind its last tile.  Barriers within.
-template <int PARTS, int LOOK>
+template <bool PACKED, int PARTS, int LOOK>
 __device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, int64_t chain, int step, int jc, int jp, float2 own,
                                        float start, float2 (&s_maps)[PARTS][CW], float2 (&s_runs)[PARTS][CW], float (&s_start)[CW]) {
     if (jp == 0 && step + 1 < ch.tiles) {
-        if (step == 0) own = make_float2(0.f, own.x * start + own.y);
+        if (step == 0) own = make_float2(0.f, pass<PACKED>(own, start));
         leave(ch.maps + (chain * ch.tiles + step) * CW + jc, own.x, own.y);
     }
     back.maps.wait(ch, jc);
-    s_maps[jp][jc] = back.maps.map();
+    s_maps[jp][jc] = back.maps.template map<PACKED>();
     if (jp == 0) s_start[jc] = start;
     __syncthreads();
     if (step >= RUN || step + 1 == RUN) {
         if (jp == 0 && step % RUN == RUN - 1 && step + 1 < ch.tiles) {
             float2 m = s_maps[0][jc];
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) m = make_float2(s_maps[i][jc].x * m.x, s_maps[i][jc].x * m.y + s_maps[i][jc].y);
-            leave(ch.runs + (chain * (ch.tiles / RUN) + step / RUN) * CW + jc, own.x * m.x, own.x * m.y + own.y);
+            for (int i = 1; i < PARTS; ++i) m = joined<PACKED>(s_maps[i][jc], m);
+            m = joined<PACKED>(own, m);
+            leave(ch.runs + (chain * (ch.tiles / RUN) + step / RUN) * CW + jc, m.x, m.y);
         }
         back.runs.wait(ch, jc);
-        s_runs[jp][jc] = back.runs.map();
+        s_runs[jp][jc] = back.runs.template map<PACKED>();
         if (jp == 0 && step >= SPAN) {
             back.state.wait(ch, jc);
             s_start[jc] = word(back.state.w[0]).y;
@@ -297,9 +312,9 @@ __device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, in
     float h = s_start[jc];
     if (step >= RUN)
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i) h = s_runs[i][jc].x * h + s_runs[i][jc].y;
+        for (int i = 0; i < PARTS; ++i) h = pass<PACKED>(s_runs[i][jc], h);
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) h = s_maps[i][jc].x * h + s_maps[i][jc].y;
+    for (int i = 0; i < PARTS; ++i) h = pass<PACKED>(s_maps[i][jc], h);
     return h;
 }
 __device__ __forceinline__ void leave_state(const Chain &ch, int64_t chain, int step, int jc, float h) {

@@ -157,6 +157,8 @@ def _plan(q, k, freq, positions, offset, interleaved, magnitude, norm=GDN2_QK_NO
     if offset:  # the shared one stays as it is
         desc = Gdn2RotaryDesc.from_buffer_copy(desc)
         desc.offset = offset
+        if desc.offset != offset:  # ctypes keeps the low 64 bits
+            raise ValueError("offset is out of range")
     return desc
 
 
@@ -209,8 +211,8 @@ def qk_norm_rotary_fwd(q, k, q_weight=None, k_weight=None, freq=None, positions=
                        magnitude=1.0, norm="rms", eps=1e-6, q_out=None, k_out=None):
     """Norm of every head of q and k, a weight, and the rotation of ``rotary_fwd``, in one pass.
 
-    norm "rms": x / sqrt(mean x^2 + eps); "l2": x / |x| (no eps; zero rows stay
-    zero).  q_weight, k_weight: [d], fp32 or bf16 (one type), None for ones.
+    norm "rms": x / sqrt(mean x^2 + eps); "l2": x / |x| (eps takes no part; zero
+    rows stay zero).  q_weight, k_weight: [d], fp32 or bf16 (one type), None for ones.
     freq None: no rotation.  Other arguments as for ``rotary_fwd``.  Returns
     (q_out, k_out).
     """

@@ -277,3 +277,25 @@ def test_captured_and_on_another_stream(g):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, both())), i
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF), (64, F32), (33, F32)])
+@pytest.mark.parametrize("norm,eps", [("rms", 1e-6), ("l2", 0.0)])
+def test_rows_that_hold_no_numbers(g, norm, eps, d, dtype):
+    # they show it, and their neighbours in the wave are as they were
+    q, k, f = rn(2, 40, 3, d, dtype=dtype), rn(2, 40, 1, d, dtype=dtype, seed=1), freqs(g, 16)
+    dy, dk = rn(2, 40, 3, d, dtype=dtype, seed=2), rn(2, 40, 1, d, dtype=dtype, seed=3)
+    want = g.qk_norm_rotary_fwd(q, k, freq=f, norm=norm, eps=eps)[0]
+    back = g.qk_norm_rotary_bwd(dy, dk, q, k, freq=f, norm=norm, eps=eps)["dq"]
+    x = q.clone()
+    x[0, 3, 1, 5] = float("nan")
+    x[1, 7, 2, 20] = float("inf")
+    keep = torch.ones(x.shape[:-1], dtype=torch.bool, device="cuda")
+    keep[0, 3, 1] = keep[1, 7, 2] = False
+    y = g.qk_norm_rotary_fwd(x, k, freq=f, norm=norm, eps=eps)[0]
+    dx = g.qk_norm_rotary_bwd(dy, dk, x, k, freq=f, norm=norm, eps=eps)["dq"]
+    assert torch.equal(y[keep], want[keep]) and torch.equal(dx[keep], back[keep])
+    assert y[0, 3, 1].isnan().all() and dx[0, 3, 1].isnan().all() and dx[1, 7, 2].isnan().all()
+    rest = torch.ones(d, dtype=torch.bool, device="cuda")
+    rest[20] = False  # inf / inf; the others are divided by it
+    assert y[1, 7, 2, 20].isnan() and (y[1, 7, 2][rest] == 0).all()

@@ -123,3 +123,48 @@ def test_one_workspace_for_many_calls(g):
         y2, S2, m2 = g.gated_scan_fwd(d["x"], d["gate"], d["s0"], return_marks=True)
         r2 = g.gated_scan_bwd(d["dy"], d["x"], d["gate"], m2, d["s0"], d["ds"])
         assert torch.equal(y, y2) and torch.equal(S, S2) and torch.equal(m, m2) and all(torch.equal(r[k], r2[k]) for k in r)
+
+
+@pytest.mark.parametrize("D", [64, 11])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_packed_sequences_keep_apart(g, D, bad):
+    # what one sequence holds reaches no other, within a tile or over many
+    lens = [50, 300, 2500, 60, 1, 4000, 7]
+    d = make(len(lens), sum(lens), D, F32, packed=True, seed=11)
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).int()
+    want = both(g, d, False, True, cu.cuda())
+    for q in (2, 5):
+        a, b = int(cu[q]), int(cu[q + 1])
+        spoilt = {n: v.clone() for n, v in d.items()}
+        for t in (a, a + 700, b - 1):
+            spoilt["x"][t] = bad
+            spoilt["dy"][t] = bad
+        spoilt["gate"][a + 5, ::2] = float("nan")
+        spoilt["gate"][b - 2, ::2] = float("nan")
+        spoilt["s0"][q] = bad
+        spoilt["ds"][q] = bad
+        got = both(g, spoilt, False, True, cu.cuda())
+        rows = torch.ones(sum(lens), dtype=torch.bool)
+        rows[a:b] = False
+        others = [i for i in range(len(lens)) if i != q]
+        assert torch.equal(got[0].cpu()[rows], want[0].cpu()[rows]) and torch.equal(got[1][others], want[1][others])
+        for n in ("dx", "d_log_decay"):
+            assert torch.equal(got[3][n].cpu()[rows], want[3][n].cpu()[rows]), n
+        assert torch.equal(got[3]["d_state0"][others], want[3]["d_state0"][others])
+        assert not got[0].cpu()[a:b].isfinite().all()
+
+
+@pytest.mark.parametrize("D", [64, 11])
+def test_marks_of_rows_outside_every_sequence_are_not_used(g, D):
+    T = 1400
+    d = make(2, T, D, F32, packed=True, seed=12)
+    cu = torch.tensor([200, 300, 900], dtype=torch.int32).cuda()
+    x = dev(d)
+    y, S, marks = g.gated_scan_fwd_varlen(x["x"], x["gate"], cu, x["s0"], return_marks=True)
+    outside = [j for j in range(11) if not 200 <= 128 * j < 900]
+    for v in (0.0, float("nan"), float("inf")):
+        marks[outside] = v
+        r = g.gated_scan_bwd_varlen(x["dy"], x["x"], x["gate"], marks, cu, x["s0"], x["ds"])
+        cut = {n: w[200:900] if n in ("x", "gate", "dy") else w for n, w in d.items()}
+        check_backward(cut, {"dx": r["dx"][200:900], "d_log_decay": r["d_log_decay"][200:900], "d_state0": r["d_state0"]},
+                       False, False, [100, 600])
