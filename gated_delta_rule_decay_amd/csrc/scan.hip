@@ -116,7 +116,10 @@ using namespace scan;
 
 bool scan_fits(const ScanArgs &a) {
     const int64_t tiles = tiles_of(a) > 0 ? tiles_of(a) : 1, blocks = (a.D + CW - 1) / CW;
-    return blocks <= (INT64_C(1) << 24) / (a.cu || a.N == 0 ? 1 : a.N) && chains_of(a) < (INT64_C(1) << 24) &&
+    // with one tile each, chains are workgroups (rounded up to whole groups) of up
+    // to 1024 lanes, and a launch of 2^32 lanes is cut short without an error
+    const int64_t most = (INT64_C(1) << 22) - GROUPS;
+    return blocks <= most / (a.cu || a.N == 0 ? 1 : a.N) && chains_of(a) < most &&
            chains_of(a) <= INT32_MAX / tiles && a.D < (INT64_C(1) << 21) &&  // 31-bit offsets within a tile
            (!a.cu || a.N * a.D < (INT64_C(1) << 29));                        // and within packed states
 }
@@ -131,8 +134,7 @@ hipError_t launch_scan_step(const ScanStepArgs &a, hipStream_t s) {
     return by_type(a.bf16, a.gate_bf16, [&](auto t, auto g) {
         using T = decltype(t);
         using G = decltype(g);
-        const int64_t lanes = vec ? a.n / 8 : a.n, grid = (lanes + 255) / 256;
-        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        const int64_t lanes = vec ? a.n / 8 : a.n, grid = (lanes + 255) / 256;  // scan_fits: under 2^28 lanes
         if (vec) hipLaunchKernelGGL((scan_step_kernel<T, G, 8>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
         else hipLaunchKernelGGL((scan_step_kernel<T, G, 1>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
         return hipGetLastError();

@@ -646,8 +646,8 @@ gdn2_status gdn2_qk_norm_bwd(const gdn2_rotary_desc *desc, const void *d_q_out, 
  * is allowed and clears the state).
  *
  * GDN2_ERR_UNSUPPORTED: a sequence of 2^31 tokens or more, 2^31 or more
- * sequences, 2^21 or more channels, 2^24 or more blocks of 64 channels over all sequences
- * (packed: over the axis), 2^31 or more of their tiles of 128 tokens, or 2^29
+ * sequences, 2^21 or more channels, 2^22 - 32 or more blocks of 64 channels over
+ * all sequences (packed: over the axis), 2^31 or more of their tiles of 128 tokens, or 2^29
  * or more values in the states of packed sequences.
  */
 typedef struct gdn2_scan_desc {

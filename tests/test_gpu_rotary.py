@@ -299,3 +299,19 @@ def test_rows_that_hold_no_numbers(g, norm, eps, d, dtype):
     rest = torch.ones(d, dtype=torch.bool, device="cuda")
     rest[20] = False  # inf / inf; the others are divided by it
     assert y[1, 7, 2, 20].isnan() and (y[1, 7, 2][rest] == 0).all()
+
+
+def test_offsets_past_32_bits(g):
+    # more than 2^31 elements a tensor
+    H, d, last = 16, 128, 37
+    T = (1 << 31) // (H * d) + last
+    q, f, w = torch.randn(1, T, H, d, dtype=BF, device="cuda"), freqs(g, d), 1 + 0.1 * rn(d, seed=1)
+    y = g.qk_norm_rotary_fwd(q, None, w, freq=f)[0]
+    turned = g.rotary_fwd(q, None, f)[0]
+    dq = g.qk_norm_rotary_bwd(y, None, q, None, w, freq=f)["dq"]
+    for first in (0, T - last):
+        sl = (slice(None), slice(first, first + last))
+        ref.check("q", y[sl], *ref.norm_turn(q[sl], w, f, None, first, False, 1.0, "rms", 1e-6))
+        ref.check("turned", turned[sl], *ref.turn_only(q[sl], f, None, first, False, 1.0))
+        dx, _, b, _ = ref.norm_turn_backward(y[sl], q[sl], w, f, None, first, False, 1.0, "rms", 1e-6)
+        ref.check("dq", dq[sl], dx, b)

@@ -1,5 +1,7 @@
 """The gated scan over chains of many tiles, whose states pass between
 workgroups."""
+import math
+
 import pytest
 import torch
 
@@ -168,3 +170,40 @@ def test_marks_of_rows_outside_every_sequence_are_not_used(g, D):
         cut = {n: w[200:900] if n in ("x", "gate", "dy") else w for n, w in d.items()}
         check_backward(cut, {"dx": r["dx"][200:900], "d_log_decay": r["d_log_decay"][200:900], "d_state0": r["d_state0"]},
                        False, False, [100, 600])
+
+
+def test_offsets_past_32_bits(g):
+    # more than 2^31 elements a tensor; a cleared state makes the last tokens a sequence of their own
+    D, last = 2048, 300
+    T = (1 << 31) // D + last
+    x = torch.randn(1, T, D, dtype=BF, device="cuda")
+    gate = -torch.rand(1, T, D, dtype=BF, device="cuda")
+    gate[0, -last] = -math.inf
+    y, S, marks = g.gated_scan_fwd(x, gate, return_marks=True)
+    head, tail = slice(0, 150), slice(T - last, T)
+    for sl in (head, tail):
+        h, b, _, _, _ = ref.forward(x[0, sl], gate[0, sl], None, False, False)
+        ref.check("y", y[0, sl], h, b)
+    r = g.gated_scan_bwd(y, x, gate, marks)
+    want = ref.backward(y[0, tail], x[0, tail], gate[0, tail], None, None, False, False)
+    for n, k in (("dx", "dx"), ("d_log_decay", "d_gate")):
+        ref.check(n, r[n][0, tail][1:], want[k][0][1:], want[k][1][1:])
+
+
+def test_many_short_sequences(g):
+    # as many workgroups as sequences, of the larger kind
+    N, T, D = 70000, 3, 5
+    d = dev(make(N, T, D, F32, seed=13))
+    y, S, m = g.gated_scan_fwd(d["x"], d["gate"], d["s0"], return_marks=True)
+    r = g.gated_scan_bwd(d["dy"], d["x"], d["gate"], m, d["s0"], d["ds"])
+    h, a = d["s0"].double(), d["gate"].double().exp()
+    for t in range(T):
+        h = a[:, t] * h + d["x"][:, t].double()
+        assert ((y[:, t].double() - h).abs() <= 2.0 ** -18 * (h.abs() + 20)).all()
+    assert torch.equal(S, y[:, -1])
+    q = d["ds"].double()
+    for t in range(T - 1, -1, -1):
+        q = d["dy"][:, t].double() + q
+        assert ((r["dx"][:, t].double() - q).abs() <= 2.0 ** -18 * (q.abs() + 20)).all()
+        q = a[:, t] * q
+    assert ((r["d_state0"].double() - q).abs() <= 2.0 ** -18 * (q.abs() + 20)).all()

@@ -153,7 +153,7 @@ def sstep(lib, d, **kw):
 
 
 BAD_SCAN = [(dict(batch=-1), SHAPE), (dict(seqlen=-1), SHAPE), (dict(dim=0), SHAPE), (dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE),
-            (dict(gate_dtype=7), DTYPE), (dict(batch=1 << 40, dim=1 << 30), SHAPE), (dict(batch=1 << 24), UNSUPPORTED),
+            (dict(gate_dtype=7), DTYPE), (dict(batch=1 << 40, dim=1 << 30), SHAPE), (dict(batch=1 << 24), UNSUPPORTED), (dict(batch=(1 << 22) - 32, dim=3), UNSUPPORTED),
             (dict(dim=1 << 30), UNSUPPORTED), (dict(dim=1 << 32, batch=1), UNSUPPORTED)]
 
 
