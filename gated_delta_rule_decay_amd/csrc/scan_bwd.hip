@@ -215,7 +215,8 @@ __global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 
 
 using namespace scan;
 
-// workgroups that run at once
+// workgroups that run at once, packed two thirds of them: a workgroup takes its
+// first tile when it starts, so those that start late find what is left
 constexpr int AT_ONCE = 768;
 
 hipError_t launch_scan_bwd(const ScanArgs &a, void *ws, hipStream_t s) {

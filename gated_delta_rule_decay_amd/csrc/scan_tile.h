@@ -7,13 +7,14 @@
 //
 // A token is the affine map h -> a h + u of a channel's state, and maps
 // compose: (a2, u2) after (a1, u1) is (a2 a1, a2 u1 + u2).  The work is cut into
-// tiles of 128 tokens and 64 channels.  A lane of a workgroup holds 32 elements
-// of a tile (8 channels of 4 tokens, or 1 of 32), composes its tokens, and the
-// groups' maps are composed over LDS; the state that enters the tile comes from
-// the tiles before it, and the lane then runs its tokens once more.  So every
-// element is read once.  Rows that are not whole aligned vectors of 8 go element
-// by element (8 x 4096 tokens of 2048 bf16 channels from an odd address: forward
-// 163 us, backward 251; aligned 96 and 149).
+// tiles of 128 tokens and 64 channels.  A lane of a workgroup holds 8 channels
+// of 4 tokens, or 1 channel of 8 (of 32, in a quarter of the lanes, would not
+// fit its registers in the backward), composes its tokens, and the groups' maps
+// are composed over LDS; the state that enters the tile comes from the tiles
+// before it, and the lane then runs its tokens once more.  So every element is
+// read once.  Rows that are not whole aligned vectors of 8 go element by element
+// (8 x 4096 tokens of 2048 bf16 channels from an odd address: forward 163 us,
+// backward 251; aligned 96 and 149).
 //
 // Bound by HBM where there are many chains; where there are few, by how long a
 // word takes from one workgroup to another, twice a tile: its run's maps, and the
@@ -27,11 +28,11 @@
 // as well, and every 256th the state behind it.  A tile composes the state, the
 // up to 15 runs and the up to 15 maps since then, always the same ones in the
 // same order, so that results do not depend on the timing; neither a map nor a
-// run waits for a state, so a chain moves on at the tiles' own pace.  A workgroup takes its tiles from a
-// counter, tokens ascending, and a tile waits only for tiles that the counter
-// gave out before it, so for workgroups that already run: the wait ends.  (It is
-// bounded all the same, for calls that share a workspace at the same time, which
-// is not allowed.)
+// run waits for a state, so a chain moves on at the tiles' own pace.  A workgroup
+// takes its tiles from a counter, along the chain, works on them in that order,
+// and a tile waits only for tiles that the counter gave out before it: the first
+// tile that is not done is at work, and the wait ends.  (It is bounded all the
+// same, for calls that share a workspace at the same time, which is not allowed.)
 //
 // Packed sequences are one axis with resets: at a sequence's first token the
 // state comes from state0, (-0, a s0 + u), and backward the gradient that enters
@@ -53,8 +54,11 @@ namespace scan {
 constexpr int CW = 64;  // channels of a workgroup: a wave's lanes in the joint
 constexpr int ROWS = SCAN_MARK;
 static_assert(ROWS == 128, "tiles are marks");
-constexpr int RUN = 16;         // tiles of a run
-constexpr int SPAN = RUN * 16;  // tiles from state to state
+// Tiles of a run, and from state to state.  (65536 tokens of 2048 channels with a
+// state behind every 16 tiles and no runs: 337 us, with runs 296; a state that
+// waits for the one before it is late for all tiles behind it.)
+constexpr int RUN = 16;
+constexpr int SPAN = RUN * 16;
 constexpr int GROUPS = 32;      // counters, each for neighbouring chains: one for all would serialise the workgroups' starts
 constexpr uint64_t NOT_YET = ~uint64_t(0);
 
