@@ -13,7 +13,7 @@
 // of k; its lanes form each (token, pair) angle once, in LDS, for all heads.
 // With 2 x 16 heads of 128 bf16 channels (a large copy: 5.14 TB/s): 65536 tokens
 // turned in 186 us, 5.8 TB/s; 32768 normed and turned in 104 us, 5.1 TB/s,
-// backward in 158 us, 5.1 TB/s.  256 tokens take 4 us on the GPU, 10 from call to
+// backward in 158 us, 5.1 TB/s.  256 tokens take 4 us on the GPU, 9 from call to
 // call, which the host needs for one.
 //
 // Angles: p f / 2 pi in fp64 (53 bits; a position of 2^20 leaves 2^-33 turns),

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(256) scan_plan_kernel(Chain ch, int64_t words,
 }
 
 // One token: bound by the launch (256 sequences of 2048 channels: 3.6 us on the
-// GPU, 8 from call to call), and by HBM with many (4096: 20 us; not in whole
+// GPU, 7 from call to call), and by HBM with many (4096: 20 us; not in whole
 // vectors 22).
 template <class T, class G, int VE>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a) {

@@ -11,7 +11,7 @@ import functools
 import math
 
 from .binding import GDN2_BF16, GDN2_F32
-from .facts import contiguous, facts, like
+from .facts import contiguous, facts, like, new_like
 from .linear import _bytes, _ptr, _register, _run, _space
 
 GDN2_ROTARY_HALF, GDN2_ROTARY_INTERLEAVED = 0, 1
@@ -166,7 +166,7 @@ def _out(given, name, x):
     if x is None:
         return None
     if given is None:
-        return x.new_empty(x.shape)
+        return new_like(x)
     like(facts(given), name, x.shape, (x.dtype,), x.device)
     return given
 
@@ -249,8 +249,8 @@ def qk_norm_rotary_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, fre
                 raise ValueError(f"{n} is missing")
             like(facts(g), n, x.shape, (q.dtype,), dev)
     dq, dk = _out(None, "dq", q), _out(None, "dk", k)
-    dqw = None if q_weight is None else q_weight.new_empty(q_weight.shape)
-    dkw = None if k_weight is None else k_weight.new_empty(k_weight.shape)
+    dqw = None if q_weight is None else new_like(q_weight)
+    dkw = None if k_weight is None else new_like(k_weight)
     ws, n = None, 0
     if dqw is not None or dkw is not None or workspace is not None:
         ws, n = _space(workspace, _sum_bytes(desc.tokens, desc.q_heads, desc.k_heads, desc.dim, desc.rotary, desc.dtype), dev)

@@ -10,7 +10,7 @@ import ctypes
 import functools
 
 from .binding import GDN2_BF16, GDN2_F32
-from .facts import facts, like
+from .facts import facts, like, new_like
 from .linear import _bytes, _ptr, _register, _run, _space
 from .rotary import _type_code
 
@@ -101,9 +101,9 @@ def _fwd(x, log_decay, cu_seqlens, state0, gate_logits, complement, out, state_o
                                      (("state0", facts(state0)), ("state_out", facts(state_out))), ("out", facts(out)))
     dev, f32 = x.device, torch.float32
     if out is None:
-        out = x.new_empty(x.shape)
+        out = new_like(x)
     if state_out is None and return_state:
-        state_out = torch.empty((N, x.shape[-1]), dtype=f32, device=dev)
+        state_out = torch.empty((N, x.shape[-1]), dtype=f32, device=dev) if state0 is None else new_like(state0)
     marks = torch.empty(mshape, dtype=f32, device=dev) if return_marks else None
     ws, n = _space(workspace, need, dev)
     if cu_seqlens is None:
@@ -149,7 +149,7 @@ def _bwd(dy, x, log_decay, marks, cu_seqlens, state0, d_state, gate_logits, comp
     like(facts(marks), "marks", mshape, (f32,), dev)
     if want_state0 is None:
         want_state0 = state0 is not None
-    dx, dg = x.new_empty(x.shape), log_decay.new_empty(x.shape)
+    dx, dg = new_like(x), new_like(log_decay)
     ds0 = torch.empty((N, x.shape[-1]), dtype=f32, device=dev) if want_state0 else None
     ws, n = _space(workspace, need, dev)
     if cu_seqlens is None:
@@ -191,6 +191,6 @@ def gated_scan_step(x, log_decay, state, gate_logits=False, complement=False, ou
     desc, _, _, _ = _request("step", facts(x), facts(log_decay), None, bool(gate_logits), bool(complement),
                              (("state", facts(state)),), ("out", facts(out)))
     if out is None:
-        out = x.new_empty(x.shape)
+        out = new_like(x)
     _run("gdn2_scan_step", x.device, desc, _ptr(x), _ptr(log_decay), _ptr(state), _ptr(out))
     return out
