@@ -5,11 +5,16 @@ namespace gdn2 {
 namespace scan {
 namespace {
 
-constexpr int NTH = 256;  // lanes of a workgroup where each holds 8 channels
+// Lanes of a workgroup.  Of single elements 1024, one workgroup a CU: twice 512,
+// of 16 tokens a lane, spill, and help only where there are many tiles (8 x 4096
+// tokens of 2047 bf16 channels 227 us for 264; 4 x 4096 of 1023 in fp32 80 for 79;
+// 20000 of 129 28 for 25).
+template <int VE>
+constexpr int lanes_of() { return VE > 1 ? 256 : 1024; }
 
 template <class T, class G, int VE, int FORM, bool PACKED>
-__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), VE > 1 ? (PACKED ? 2 : 3) : 4) scan_bwd_kernel(ScanArgs a, Chain ch) {
-    using Q = Lanes<VE, NTH>;
+__global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4) scan_bwd_kernel(ScanArgs a, Chain ch) {
+    using Q = Lanes<VE, lanes_of<VE>()>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
     __shared__ float2 s_map[Q::GRP][Q::ROW], s_rev[Q::GRP][Q::ROW];
     __shared__ float2 s_part[PARTS][CW], s_rpart[PARTS][CW], s_maps[PARTS][CW], s_runs[PARTS][CW];
@@ -229,7 +234,7 @@ hipError_t launch_scan_bwd(const ScanArgs &a, void *ws, hipStream_t s) {
         using T = decltype(t);
         using G = decltype(g);
         constexpr int VE = decltype(ve)::value, FORM = decltype(form)::value;
-        const dim3 grid(grid_of(ch, AT_ONCE)), block(Lanes<VE, NTH>::NTH);
+        const dim3 grid(grid_of(ch, AT_ONCE)), block(lanes_of<VE>());
         if (a.cu) hipLaunchKernelGGL((scan_bwd_kernel<T, G, VE, FORM, true>), grid, block, 0, s, a, ch);
         else hipLaunchKernelGGL((scan_bwd_kernel<T, G, VE, FORM, false>), grid, block, 0, s, a, ch);
         return hipGetLastError();

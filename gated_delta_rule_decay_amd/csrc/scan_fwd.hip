@@ -5,7 +5,11 @@ namespace gdn2 {
 namespace scan {
 namespace {
 
-constexpr int NTH = 256;  // lanes of a workgroup where each holds 8 channels
+// Lanes of a workgroup.  Of single elements 512 lanes fit a CU twice (8 x 4096
+// tokens of 2047 bf16 channels: 151 us, with 1024 lanes 184; 4 x 4096 of 1023 in
+// fp32 54 and 59); packed, with what each token is, they would spill.
+template <int VE, bool PACKED>
+constexpr int lanes_of() { return VE > 1 ? 256 : PACKED ? 1024 : 512; }
 
 // Workgroups of a CU.  Three, where their registers hold the next tile as well;
 // packed tiles of 6 or 8 bytes an element would spill (7 sequences, 32768 tokens
@@ -15,8 +19,8 @@ template <class T, class G, bool PACKED>
 constexpr int per_cu() { return PACKED && sizeof(T) + sizeof(G) > 4 ? 2 : 3; }
 
 template <class T, class G, int VE, int FORM, bool PACKED>
-__global__ void __launch_bounds__((Lanes<VE, NTH>::NTH), (VE > 1 ? per_cu<T, G, PACKED>() : 4)) scan_fwd_kernel(ScanArgs a, Chain ch) {
-    using Q = Lanes<VE, NTH>;
+__global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, G, PACKED>() : 4)) scan_fwd_kernel(ScanArgs a, Chain ch) {
+    using Q = Lanes<VE, lanes_of<VE, PACKED>()>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
     __shared__ float2 s_map[Q::GRP][Q::ROW];  // groups' maps, then .y the state that enters
     __shared__ float2 s_part[PARTS][CW], s_maps[PARTS][CW], s_runs[PARTS][CW];
@@ -195,7 +199,7 @@ hipError_t launch_scan_fwd(const ScanArgs &a, void *ws, hipStream_t s) {
         using T = decltype(t);
         using G = decltype(g);
         constexpr int VE = decltype(ve)::value, FORM = decltype(form)::value;
-        const dim3 grid(grid_of(ch, AT_ONCE)), block(Lanes<VE, NTH>::NTH);
+        const dim3 grid(grid_of(ch, AT_ONCE)), block(a.cu ? lanes_of<VE, true>() : lanes_of<VE, false>());
         if (a.cu) hipLaunchKernelGGL((scan_fwd_kernel<T, G, VE, FORM, true>), grid, block, 0, s, a, ch);
         else hipLaunchKernelGGL((scan_fwd_kernel<T, G, VE, FORM, false>), grid, block, 0, s, a, ch);
         return hipGetLastError();

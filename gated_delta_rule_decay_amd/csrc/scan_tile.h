@@ -8,12 +8,12 @@
 // A token is the affine map h -> a h + u of a channel's state, and maps
 // compose: (a2, u2) after (a1, u1) is (a2 a1, a2 u1 + u2).  The work is cut into
 // tiles of 128 tokens and 64 channels.  A lane of a workgroup holds 8 channels
-// of 4 tokens, or 1 channel of 8 (of 32, in a quarter of the lanes, would not
-// fit its registers in the backward), composes its tokens, and the groups' maps
+// of 4 tokens, or 1 channel of 8 or 16 (of 32, in 256 lanes, would not fit its
+// registers in the backward), composes its tokens, and the groups' maps
 // are composed over LDS; the state that enters the tile comes from the tiles
 // before it, and the lane then runs its tokens once more.  So every element is
 // read once.  Rows that are not whole aligned vectors of 8 go element by element
-// (8 x 4096 tokens of 2048 bf16 channels from an odd address: forward 163 us,
+// (8 x 4096 tokens of 2048 bf16 channels from an odd address: forward 121 us,
 // backward 251; aligned 96 and 149).
 //
 // Bound by HBM where there are many chains; where there are few, by how long a
@@ -114,7 +114,7 @@ namespace {
 // A workgroup's lanes: VE channels of K neighbouring tokens each.
 template <int VE, int N>
 struct Lanes {
-    static constexpr int NTH = VE > 1 ? N : 1024;
+    static constexpr int NTH = N;
     static constexpr int LPR = CW / VE;          // lanes of a row
     static constexpr int GRP = NTH / LPR;        // groups of rows
     static constexpr int K = ROWS / GRP;         // rows of a group
