@@ -28,12 +28,12 @@ __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4)
     // packed: the states of the sequences
     const auto b0 = buffer<float>(a.s0, 0, PACKED && a.s0 ? states * D : 0), bd = buffer<float>(a.d_sT, 0, PACKED && a.d_sT ? states * D : 0);
 
-    if (threadIdx.x == 0) s_take = take(ch, true);
+    if (jp == 0) s_take = __builtin_amdgcn_readfirstlane(take(ch, true));
     __syncthreads();
     int tile = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take));
     while (tile >= 0) {
         unsigned next = 0;
-        if (threadIdx.x == 0) next = take(ch, false);
+        if (jp == 0) next = take(ch, false);
         // steps of a chain go from its last tile to its first
         const Spot p = spot_of<PACKED>(ch, a.T, blocks, tile, true);
         const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4)
                 gl[e] = rv[e] * (H[k][e] - (form.comp ? x[k][e] : 0.f));
                 if (form.logits) gl[e] *= -w;
             }
-            store_row<T, VE>(bdx, rw.live(k) ? at(k, sizeof(T)) : NOWHERE, gx);
-            store_row<G, VE>(bdg, rw.live(k) ? at(k, sizeof(G)) : NOWHERE, gl);
-            if (starts) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.first(k), D, c4) : g * K + k == 0 ? c4 : NOWHERE, rv);
+            store_row<T, VE>(bdx, only(rw.live(k), at(k, sizeof(T))), gx);
+            store_row<G, VE>(bdg, only(rw.live(k), at(k, sizeof(G))), gl);
+            if (starts) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.first(k), D, c4) : only(g * K + k == 0, c4), rv);
         }
     }
 }

@@ -48,9 +48,9 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
         ahead.load(ch.seq, p.row, g * K, p.rows);
     };
 
-    if (threadIdx.x == 0) {
-        s_take[0] = take(ch, true);
-        s_take[1] = take(ch, false);
+    if (jp == 0) {
+        s_take[0] = __builtin_amdgcn_readfirstlane(take(ch, true));
+        s_take[1] = __builtin_amdgcn_readfirstlane(take(ch, false));
     }
     __syncthreads();
     int tile = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take[0])), after = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take[1]));
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): in the loop the loads are waited for over the stores behind them
     while (tile >= 0) {
         unsigned next = 0;
-        if (threadIdx.x == 0) next = take(ch, false);
+        if (jp == 0) next = take(ch, false);
         const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
         const int64_t base = p.row * a.D;
         auto at = [&](int k, unsigned size) { return (c < D ? lane * size : NOWHERE) + k * D * size; };
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
                     A[k][e] = rw.first(k) ? RESET : A[k][e];
                 }
                 // here, not below: another wave may end this sequence, and state_out may be state0
-                if (k == 0) store_row<float, VE>(bm, g == 0 && rw.first(0) ? c4 : NOWHERE, m);
+                if (k == 0) store_row<float, VE>(bm, only((g == 0) & rw.first(0), c4), m);
             }
         }
         {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
         float hv[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) hv[e] = s_map[g][Q::place(l, e)].y;
-        if (marked) store_row<float, VE>(bm, g == 0 && rw.live(0) && !rw.first(0) ? c4 : NOWHERE, hv);
+        if (marked) store_row<float, VE>(bm, only((g == 0) & rw.live(0) & !rw.first(0), c4), hv);
         // the state behind the last token, in the wave that holds it; packed: behind each sequence's last
         const bool ends = a.s_out != nullptr && (PACKED ? edges : p.step == ch.tiles - 1);
         const auto bs = PACKED ? buffer<float>(a.s_out, 0, states * D) : buffer<float>(a.s_out, p.sequence * a.D, D);
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
                 const float h = A[k][e] * hv[e] + U[k][e];
                 hv[e] = rw.first(k) ? U[k][e] : h;
             }
-            store_row<T, VE>(by, rw.live(k) ? at(k, sizeof(T)) : NOWHERE, hv);
-            if (ends) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.last(k), D, c4) : g * K + k == p.rows - 1 ? c4 : NOWHERE, hv);
+            store_row<T, VE>(by, only(rw.live(k), at(k, sizeof(T))), hv);
+            if (ends) store_row<float, VE>(bs, PACKED ? rw.state(k, rw.last(k), D, c4) : only(g * K + k == p.rows - 1, c4), hv);
         }
         p = q;
     }

@@ -171,16 +171,15 @@ __device__ __forceinline__ unsigned group_of(const Chain &ch) {
     return (blockIdx.x + (ch.tiles > 1 ? blockIdx.x / 256 * 11 : 0)) % ch.groups;
 }
 // A workgroup's next number from its counter (without counters: its own, once),
-// and the tile that it stands for, -1 behind the last.
-// (of one lane)
+// in the first lane of a wave that asks as a whole: the others add to nowhere.
+// (A branch of one lane would let the compiler move what is live around it while
+// the other lanes are off.)
 __device__ __forceinline__ unsigned take(const Chain &ch, bool start) {
     if (ch.tiles == 1) return start ? blockIdx.x / ch.groups : INT32_MAX;
-    // an address that looks like the lane's own: at a common one the compiler
-    // adds for the whole wave, and waits for the result on the spot
-    unsigned zero = 0;
-    asm volatile("" : "+v"(zero));
-    return __hip_atomic_fetch_add(ch.counters + group_of(ch) * COUNTER_STEP + zero, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const auto b = buffer<unsigned>(ch.counters, group_of(ch) * COUNTER_STEP, 1);
+    return __builtin_amdgcn_raw_ptr_buffer_atomic_add_i32(1, b, threadIdx.x % 64 ? NOWHERE : 0, 0, 0);
 }
+// The tile that a number stands for, -1 behind the last.
 __device__ __forceinline__ int tile_of(const Chain &ch, unsigned i) {
     // a group's chains neighbour each other: they share lines of their rows
     // (65536 rows of 4 KB copied in tiles: 5.45 TB/s, with every 8th block of
@@ -336,6 +335,11 @@ __device__ __forceinline__ void leave_state(const Chain &ch, int64_t chain, int 
 // No lane of the kernels branches by itself while a tile is in registers: what
 // a lane does not need goes to NOWHERE, and branches are those of whole waves.
 
+// An offset, or nowhere.  (By its top bit, which no offset has: of a ?: the
+// compiler makes a branch where it is used more than once.)
+__device__ __forceinline__ unsigned only(bool on, unsigned at) { return at | static_cast<unsigned>(!on) << 31; }
+static_assert(NOWHERE == 1u << 31, "nowhere is a bit");
+
 // VE elements of a row as stored.
 template <class E, int VE>
 struct Row {
@@ -421,15 +425,16 @@ struct Rows {
     __device__ __forceinline__ bool edges() const {
         bool edge = false;
 #pragma unroll
-        for (int k = 0; k < K; ++k) edge = edge || first(k) || last(k);
+        for (int k = 0; k < K; ++k) edge = edge | first(k) | last(k);
         return __builtin_amdgcn_ballot_w64(edge) != 0;
     }
     __device__ __forceinline__ bool live(int k) const { return sq[k + 1] != 0; }
-    __device__ __forceinline__ bool first(int k) const { return PACKED && live(k) && sq[k] != sq[k + 1]; }
-    __device__ __forceinline__ bool last(int k) const { return PACKED && live(k) && sq[k + 2] != sq[k + 1]; }
+    __device__ __forceinline__ bool first(int k) const { return PACKED & live(k) & (sq[k] != sq[k + 1]); }
+    __device__ __forceinline__ bool last(int k) const { return PACKED & live(k) & (sq[k + 2] != sq[k + 1]); }
     // offset of the row's sequence in states [N, D] for a channel's byte offset, or nowhere
+    // (of no sequence: -4 D, which stays below 2^32 with a vector added)
     __device__ __forceinline__ unsigned state(int k, bool on, unsigned D, unsigned c4) const {
-        return on ? static_cast<unsigned>(sq[k + 1] - 1) * (D * 4) + c4 : NOWHERE;
+        return only(on, static_cast<unsigned>(sq[k + 1] - 1) * (D * 4) + c4);
     }
 };
 
