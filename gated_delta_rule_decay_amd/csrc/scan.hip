@@ -60,7 +60,9 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a) {
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
         const float v = a.logits ? small_of_logit(g[e]) : small_of_log(g[e]);
-        h[e] = decay_of(v) * s[e] + (a.comp ? rest_of(v) * x[e] : x[e]);
+        const float u = a.comp ? rest_of(v) * x[e] : x[e];
+        // of a decay near 1 by its complement: a state passes this rounding once a token
+        h[e] = __float_as_int(v) < 0 ? s[e] + (u - rest_of(v) * s[e]) : v * s[e] + u;
     }
     store_row<float, VE>(bs, i * 4, h);
     store_row<T, VE>(buffer<T>(a.y, first, n), i * sizeof(T), h);

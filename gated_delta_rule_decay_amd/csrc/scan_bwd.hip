@@ -16,6 +16,7 @@ template <class T, class G, int VE, int FORM, bool PACKED>
 __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4) scan_bwd_kernel(ScanArgs a, Chain ch) {
     using Q = Lanes<VE, lanes_of<VE>()>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
+    // groups' maps: (factor, addend) and (its complement, addend backward), then .y what enters
     __shared__ float2 s_map[Q::GRP][Q::ROW], s_rev[Q::GRP][Q::ROW];
     __shared__ float2 s_part[PARTS][CW], s_rpart[PARTS][CW], s_maps[PARTS][CW], s_runs[PARTS][CW];
     __shared__ float s_start[CW];
@@ -71,90 +72,92 @@ __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4)
         }
         const bool edges = PACKED && rw.edges();
         {
-            // maps of the group: forward (fa, fu), backward (ra, ru)
-            float fa[VE], fu[VE], ra[VE], ru[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                fa[e] = ra[e] = 1.f;
-                fu[e] = ru[e] = 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float h0[VE], d0[VE];
-#pragma unroll
-                for (int e = 0; e < VE; ++e) h0[e] = d0[e] = 0.f;
-                if (PACKED && edges) {
-                    Row<float, VE> i, o;
-                    i.load(b0, rw.state(k, rw.first(k), D, c4));
-                    o.load(bd, rw.state(k, rw.last(k), D, c4));
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        h0[e] = i[e];
-                        d0[e] = o[e];
-                    }
+            // maps of the group: the same decays (as in Joint), addends forward and backward
+            struct Both { float a = 1.f, rest = 0.f, fu = 0.f, ru = 0.f; };
+            bool starts = false, ends = false;  // whether a sequence does, in the group's tokens so far
+            auto token = [&](Both &m, int k, int e, float h0, float d0) {
+                const float v = rw.live(k) ? V[k][e] : -0.f;  // a = 1, w = 0
+                const float f = decay_of(v), w = rest_of(v);
+                float u = form.comp ? w * x[k][e] : x[k][e], y = dy[k][e];
+                if (PACKED) {  // else what is behind a sequence's end reads as zero
+                    u = rw.live(k) ? u + f * h0 : 0.f;
+                    y = rw.live(k) ? y + d0 : 0.f;
                 }
+                const float h = f * m.fu + u, r = m.a * (f * y) + m.ru;
+                m.fu = rw.first(k) ? u : h;
+                // from right to left: the tokens so far come after this one's r
+                m.ru = ends ? m.ru : r;
+                m.rest += w * m.a;
+                m.a *= f;
+            };
+            auto put = [&](const Both &m, int e) {
+                s_map[g][Q::place(l, e)] = make_float2(PACKED ? with_mark(m.a, starts) : m.a, m.fu);
+                s_rev[g][Q::place(l, e)] = make_float2(PACKED ? with_mark(m.rest, ends) : m.rest, m.ru);
+            };
+            if constexpr (PACKED) {
+                Both m[VE];
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    Row<float, VE> h0 = {}, d0 = {};
+                    if (edges) {
+                        h0.load(b0, rw.state(k, rw.first(k), D, c4));
+                        d0.load(bd, rw.state(k, rw.last(k), D, c4));
+                    }
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) token(m[e], k, e, h0[e], d0[e]);
+                    starts = starts | rw.first(k);
+                    ends = ends | rw.last(k);
+                }
+#pragma unroll
+                for (int e = 0; e < VE; ++e) put(m[e], e);
+            } else {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float f = rw.live(k) ? decay_of(V[k][e]) : 1.f;
-                    float u = form.comp ? rest_of(V[k][e]) * x[k][e] : x[k][e], y = dy[k][e];
-                    if (PACKED) {
-                        u += f * h0[e];
-                        y += d0[e];
-                    }
-                    u = rw.live(k) ? u : 0.f;
-                    y = rw.live(k) ? y : 0.f;
-                    const float h = f * fu[e] + u;
-                    fu[e] = rw.first(k) ? u : h;
-                    fa[e] = rw.first(k) ? RESET : fa[e] * f;
-                    // from right to left: the tokens so far come after this one's r
-                    const float2 n = joined<PACKED>(make_float2(ra[e], ru[e]), make_float2(rw.last(k) ? RESET : f, f * y));
-                    ra[e] = n.x;
-                    ru[e] = n.y;
-                }
-            }
+                    Both m;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                s_map[g][Q::place(l, e)] = make_float2(fa[e], fu[e]);
-                s_rev[g][Q::place(l, e)] = make_float2(ra[e], ru[e]);
+                    for (int k = 0; k < K; ++k) token(m, k, e, 0.f, 0.f);
+                    put(m, e);
+                }
             }
         }
         __syncthreads();
         if (jp == 0) s_take = __builtin_amdgcn_readfirstlane(next);
         {
-            float2 m = make_float2(1.f, 0.f), n = make_float2(1.f, 0.f);
+            Joint<PACKED> m, n;
 #pragma unroll 4
             for (int i = 0; i < Q::PER; ++i) {
                 const float2 f = s_map[jp * Q::PER + i][jc], b = s_rev[jp * Q::PER + i][jc];
-                m = joined<PACKED>(f, m);
-                n = joined<PACKED>(n, b);
+                m.then(fabsf(f.x), fabsf(b.x), f.y, PACKED && has_mark(f.x));
+                n.behind(fabsf(f.x), fabsf(b.x), b.y, PACKED && has_mark(b.x));
             }
-            s_part[jp][jc] = m;
-            s_rpart[jp][jc] = n;
+            s_part[jp][jc] = m.map();
+            s_rpart[jp][jc] = n.map();
         }
         __syncthreads();
         tile = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take));
         float r = r0;
         if (ch.tiles > 1) {
-            float2 n = s_rpart[0][jc];
+            Joint<PACKED> n;
+            if (jp == 0)
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) n = joined<PACKED>(n, s_rpart[i][jc]);
+                for (int i = 0; i < PARTS; ++i) n.behind(s_rpart[i][jc]);
             LookBack<Q::LOOK> back;
             back.start(ch, p.chain, p.step, jc, jp);
-            r = enter<PACKED, PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, n, r0, s_maps, s_runs, s_start);
+            r = enter<PACKED, PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, n.map(), r0, s_maps, s_runs, s_start);
         }
         for (int i = 0; i < jp; ++i) h = pass<PACKED>(s_part[i][jc], h);
         for (int i = PARTS - 1; i > jp; --i) r = pass<PACKED>(s_rpart[i][jc], r);
 #pragma unroll
         for (int i = 0; i < Q::PER; ++i) {
             float2 &m = s_map[jp * Q::PER + i][jc];
-            const float next_h = pass<PACKED>(m, h);
+            const float through = fabsf(m.x) * h + m.y, next_h = PACKED && has_mark(m.x) ? m.y : through;
             m.y = h;
             h = next_h;
         }
 #pragma unroll
         for (int i = Q::PER - 1; i >= 0; --i) {
             float2 &m = s_rev[jp * Q::PER + i][jc];
-            const float next_r = pass<PACKED>(m, r);
+            const float through = fabsf(s_map[jp * Q::PER + i][jc].x) * r + m.y, next_r = PACKED && has_mark(m.x) ? m.y : through;
             m.y = r;
             r = next_r;
         }
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4)
 #pragma unroll
             for (int e = 0; e < VE; ++e) settle(V[k][e]);
         const auto bdx = buffer<T>(a.dx, base, p.rows * D), bdg = buffer<G>(a.d_gate, base, p.rows * D);
-        float H[K][VE], rv[VE];  // H: the states that enter the tokens
+        float H[K][VE], rv[VE];  // H: the states that enter the tokens, then what d log a_t takes of them
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             H[0][e] = s_map[g][Q::place(l, e)].y;
@@ -180,10 +183,12 @@ __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) H[k][e] = rw.first(k) ? i[e] : H[k][e];
             }
-            if (k + 1 < K)
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    H[k + 1][e] = decay_of(V[k][e]) * H[k][e] + (form.comp ? rest_of(V[k][e]) * x[k][e] : x[k][e]);
+            for (int e = 0; e < VE; ++e) {
+                if (k + 1 < K) H[k + 1][e] = decay_of(V[k][e]) * H[k][e] + (form.comp ? rest_of(V[k][e]) * x[k][e] : x[k][e]);
+                if (form.comp) H[k][e] -= x[k][e];
+                settle(H[k][e]);
+            }
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4)
                 const float w = rest_of(V[k][e]), s = dy[k][e] + rv[e];
                 rv[e] = rw.live(k) ? decay_of(V[k][e]) * s : rv[e];
                 gx[e] = form.comp ? w * s : s;
-                gl[e] = rv[e] * (H[k][e] - (form.comp ? x[k][e] : 0.f));
+                gl[e] = rv[e] * H[k][e];
                 if (form.logits) gl[e] *= -w;
             }
             store_row<T, VE>(bdx, only(rw.live(k), at(k, sizeof(T))), gx);

@@ -23,6 +23,7 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
     using Q = Lanes<VE, lanes_of<VE, PACKED>()>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
     __shared__ float2 s_map[Q::GRP][Q::ROW];  // groups' maps, then .y the state that enters
+    __shared__ float s_rest[Q::GRP][Q::ROW];
     __shared__ float2 s_part[PARTS][CW], s_maps[PARTS][CW], s_runs[PARTS][CW];
     __shared__ float s_start[CW];
     __shared__ unsigned s_take[2];
@@ -64,18 +65,27 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
         const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
         const int64_t base = p.row * a.D;
         auto at = [&](int k, unsigned size) { return (c < D ? lane * size : NOWHERE) + k * D * size; };
-        float A[K][VE], U[K][VE];
+        float A[K][VE], U[K][VE], F[VE], R[VE];  // F, R: the factor of the group's map, and its complement (as in Joint)
         const Rows<K, PACKED> rw = ahead;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int e = 0; e < VE; ++e) {
+            F[e] = 1.f;
+            R[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float v = form.logits ? small_of_logit(gt[k][e]) : small_of_log(gt[k][e]);
+            for (int k = 0; k < K; ++k) {
+                float v = form.logits ? small_of_logit(gt[k][e]) : small_of_log(gt[k][e]);
+                v = rw.live(k) ? v : -0.f;  // a = 1, w = 0
+                const float w = rest_of(v), u = form.comp ? w * x[k][e] : x[k][e];
                 A[k][e] = decay_of(v);
-                U[k][e] = form.comp ? rest_of(v) * x[k][e] : x[k][e];
+                U[k][e] = PACKED ? (rw.live(k) ? u : 0.f) : u;  // x behind a sequence's end reads as zero
+                R[e] += w * F[e];
+                F[e] *= A[k][e];
                 settle(A[k][e]);
                 settle(U[k][e]);
             }
+            settle(F[e]);
+            settle(R[e]);
+        }
         const bool edges = PACKED && rw.edges();
         float h0 = 0.f;
         if (!PACKED && p.step == 0) {  // what the chain starts from
@@ -98,49 +108,52 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
                 for (int e = 0; e < VE; ++e) {
                     m[e] = h0[e];
                     U[k][e] += A[k][e] * m[e];
-                    A[k][e] = rw.first(k) ? RESET : A[k][e];
                 }
                 // here, not below: another wave may end this sequence, and state_out may be state0
                 if (k == 0) store_row<float, VE>(bm, only((g == 0) & rw.first(0), c4), m);
             }
         }
         {
-            float ca[VE], cu[VE];
+            float cu[VE];
+            bool starts = false;  // whether a sequence does within the group
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                ca[e] = 1.f;
-                cu[e] = 0.f;
-            }
+            for (int k = 0; k < K; ++k) starts = starts | rw.first(k);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) cu[e] = 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    A[k][e] = rw.live(k) ? A[k][e] : 1.f;
-                    U[k][e] = rw.live(k) ? U[k][e] : 0.f;
                     const float u = A[k][e] * cu[e] + U[k][e];
                     cu[e] = rw.first(k) ? U[k][e] : u;
-                    ca[e] = rw.first(k) ? RESET : ca[e] * A[k][e];
                 }
 #pragma unroll
-            for (int e = 0; e < VE; ++e) s_map[g][Q::place(l, e)] = make_float2(ca[e], cu[e]);
+            for (int e = 0; e < VE; ++e) {
+                s_map[g][Q::place(l, e)] = make_float2(PACKED ? with_mark(F[e], starts) : F[e], cu[e]);
+                s_rest[g][Q::place(l, e)] = R[e];
+            }
         }
         __syncthreads();
         if (jp == 0) s_take[0] = __builtin_amdgcn_readfirstlane(next);
         {
-            float2 m = make_float2(1.f, 0.f);
+            Joint<PACKED> m;
 #pragma unroll
-            for (int i = 0; i < Q::PER; ++i) m = joined<PACKED>(s_map[jp * Q::PER + i][jc], m);
-            s_part[jp][jc] = m;
+            for (int i = 0; i < Q::PER; ++i) {
+                const float2 n = s_map[jp * Q::PER + i][jc];
+                m.then(fabsf(n.x), s_rest[jp * Q::PER + i][jc], n.y, PACKED && has_mark(n.x));
+            }
+            s_part[jp][jc] = m.map();
         }
         __syncthreads();
         tile = after;
         after = tile_of(ch, __builtin_amdgcn_readfirstlane(s_take[0]));
         float h = h0;
         if (ch.tiles > 1) {
-            float2 m = s_part[0][jc];
+            Joint<PACKED> m;
+            if (jp == 0)
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) m = joined<PACKED>(s_part[i][jc], m);
-            h = enter<PACKED, PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, m, h0, s_maps, s_runs, s_start);
+                for (int i = 0; i < PARTS; ++i) m.then(s_part[i][jc]);
+            h = enter<PACKED, PARTS, Q::LOOK>(ch, back, p.chain, p.step, jc, jp, m.map(), h0, s_maps, s_runs, s_start);
         }
         // The next tile's loads are in flight from here to the next round; behind
         // the last tile they read zeros.  (From before the wait for the words,
@@ -153,7 +166,7 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
 #pragma unroll
         for (int i = 0; i < Q::PER; ++i) {
             float2 &m = s_map[jp * Q::PER + i][jc];
-            const float next_h = pass<PACKED>(m, h);
+            const float through = fabsf(m.x) * h + m.y, next_h = PACKED && has_mark(m.x) ? m.y : through;
             m.y = h;
             h = next_h;
         }

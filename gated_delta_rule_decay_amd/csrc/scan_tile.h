@@ -137,10 +137,13 @@ struct Form {
         : comp(FORM == ANY ? a.comp != 0 : (FORM & 1) != 0), logits(FORM == ANY ? a.logits != 0 : (FORM & 2) != 0) {}
 };
 
-// A decay a and its complement w = 1 - a in one float: the smaller one, which
-// is known to its last bits, with the sign set where it is w.  The other is its
-// difference from 1, rounded once; near a = 1, where memories are long, an
-// error of a counts once for each token that they span.
+// A decay a and its complement w = 1 - a in one float: the smaller one, with
+// the sign set where it is w.  The other is its difference from 1, rounded once.
+// (The smaller one is as near as its exponential: from a logarithm within some
+// roundings, from a logit g within 2 |g| of them, those of g log2(e).)  Near a = 1
+// the rounded a is off by much of w, always to the same side where gates do not
+// change: it only multiplies states for the tokens of one lane, and what passes
+// between lanes is joined by complements (Joint).
 __device__ __forceinline__ float decay_of(float v) {
     return __float_as_int(v) < 0 ? 1.f - fabsf(v) : v;
 }
@@ -191,19 +194,56 @@ __device__ __forceinline__ int tile_of(const Chain &ch, unsigned i) {
         step < static_cast<unsigned>(ch.tiles) ? static_cast<int>(step * ch.chains + first + i - step * mine) : -1);
 }
 
-// Maps (factor, addend): `n` after `m`, and of a state.
+// A map: (factor, addend), the factor held as a decay is (decay_of), except that
+// where 1 - a is 0 it is a = 1, so that -0 stays free for a reset.
 constexpr float RESET = -0.f;
 __device__ __forceinline__ bool resets(float factor) { return __float_as_uint(factor) == 0x80000000u; }
+__device__ __forceinline__ float factor_of(float a, float rest) {
+    return __float_as_uint(rest) - 1u < 0x3effffffu ? -rest : a;  // 0 < rest < 0.5
+}
+// what a map makes of a state
 template <bool PACKED>
 __device__ __forceinline__ float pass(float2 n, float h) {
-    const float through = n.x * h + n.y;
+    const float through = decay_of(n.x) * h + n.y;
     return PACKED && resets(n.x) ? n.y : through;
 }
+// Maps joined one by one: the product of their factors, and its complement as a
+// sum of complements, 1 - a2 a1 = (1 - a1) + (1 - a2) a1: of products of rounded
+// factors it would be off by as much as 1 - a is where all are near 1, and by
+// the same on every tile that a state passes.  (One sequence, a = 1 - 6e-6 on each
+// of 65536 tokens: off by up to 1.5e-3 of its largest value that way, with the
+// sum 2.4e-6.)
 template <bool PACKED>
-__device__ __forceinline__ float2 joined(float2 n, float2 m) {
-    const float u = pass<PACKED>(n, m.y), a = n.x * m.x;
-    return make_float2(PACKED && resets(n.x) ? RESET : a, u);
+struct Joint {
+    float a = 1.f, rest = 0.f, u = 0.f;
+    // (f, w, v, cut): a factor, its complement, an addend, and whether the map resets
+    __device__ __forceinline__ void then(float f, float w, float v, bool cut) {  // after the maps so far
+        w = w * a + rest;
+        const float h = f * u + v;
+        rest = cut ? 1.f : w;
+        u = cut ? v : h;
+        a = cut ? RESET : a * f;
+    }
+    __device__ __forceinline__ void behind(float f, float w, float v, bool cut) {  // before the maps so far
+        const bool done = PACKED && resets(a);
+        w = w * a + rest;
+        const float h = a * v + u;
+        rest = (done | cut) ? 1.f : w;
+        u = done ? u : h;
+        a = (done | cut) ? RESET : a * f;
+    }
+    __device__ __forceinline__ void then(float2 n) { then(decay_of(n.x), rest_of(n.x), n.y, PACKED && resets(n.x)); }
+    __device__ __forceinline__ void behind(float2 n) { behind(decay_of(n.x), rest_of(n.x), n.y, PACKED && resets(n.x)); }
+    __device__ __forceinline__ float2 map() const { return make_float2(factor_of(a, rest), u); }
+};
+
+// The map of a group of tokens, with its factor and the complement apart: the
+// top bit of `value` set where the map resets (by itself, so that a decay that is
+// no number has no such bit).
+__device__ __forceinline__ float with_mark(float value, bool cut) {
+    return __uint_as_float((__float_as_uint(value) & 0x7fffffffu) | static_cast<unsigned>(cut) << 31);
 }
+__device__ __forceinline__ bool has_mark(float value) { return __float_as_int(value) < 0; }
 
 // A channel's word: (factor, addend) of a map, or (anything, state).
 __device__ __forceinline__ void leave(uint64_t *p, float a, float u) {
@@ -268,10 +308,10 @@ struct Look {
     // the words' map
     template <bool PACKED>
     __device__ __forceinline__ float2 map() const {
-        float2 m = make_float2(1.f, 0.f);
+        Joint<PACKED> m;
 #pragma unroll
-        for (int k = 0; k < LOOK; ++k) m = joined<PACKED>(want(k) ? word(w[k]) : make_float2(1.f, 0.f), m);
-        return m;
+        for (int k = 0; k < LOOK; ++k) m.then(want(k) ? word(w[k]) : make_float2(1.f, 0.f));
+        return m.map();
     }
 };
 
@@ -306,11 +346,12 @@ __device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, in
     __syncthreads();
     if (step >= RUN || step + 1 == RUN) {
         if (jp == 0 && step % RUN == RUN - 1 && step + 1 < ch.tiles) {
-            float2 m = s_maps[0][jc];
+            Joint<PACKED> m;
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) m = joined<PACKED>(s_maps[i][jc], m);
-            m = joined<PACKED>(own, m);
-            leave(ch.runs + (chain * (ch.tiles / RUN) + step / RUN) * CW + jc, m.x, m.y);
+            for (int i = 0; i < PARTS; ++i) m.then(s_maps[i][jc]);
+            m.then(own);
+            const float2 run = m.map();
+            leave(ch.runs + (chain * (ch.tiles / RUN) + step / RUN) * CW + jc, run.x, run.y);
         }
         back.runs.wait(ch, jc);
         s_runs[jp][jc] = back.runs.template map<PACKED>();
