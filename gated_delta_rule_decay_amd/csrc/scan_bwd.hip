@@ -12,8 +12,14 @@ namespace {
 template <int VE>
 constexpr int lanes_of() { return VE > 1 ? 256 : 1024; }
 
+// Workgroups of a CU: three, packed two, where three would spill 34 to 72 registers
+// (7 sequences, 32768 tokens of 2048 channels: bf16 230 us with two, 288 with
+// three; fp32 339 and 452).
+template <int VE, bool PACKED>
+constexpr int per_cu() { return VE > 1 ? (PACKED ? 2 : 3) : 4; }  // (of single elements: sixteen waves, one workgroup)
+
 template <class T, class G, int VE, int FORM, bool PACKED>
-__global__ void __launch_bounds__(lanes_of<VE>(), VE > 1 ? (PACKED ? 2 : 3) : 4) scan_bwd_kernel(ScanArgs a, Chain ch) {
+__global__ void __launch_bounds__(lanes_of<VE>(), (per_cu<VE, PACKED>())) scan_bwd_kernel(ScanArgs a, Chain ch) {
     using Q = Lanes<VE, lanes_of<VE>()>;
     constexpr int K = Q::K, PARTS = Q::PARTS;
     // groups' maps: (factor, addend) and (its complement, addend backward), then .y what enters

@@ -11,12 +11,12 @@ namespace {
 template <int VE, bool PACKED>
 constexpr int lanes_of() { return VE > 1 ? 256 : PACKED ? 1024 : 512; }
 
-// Workgroups of a CU.  Three, where their registers hold the next tile as well;
-// packed tiles of 6 or 8 bytes an element would spill (7 sequences, 32768 tokens
-// of 2048 channels: bf16 with fp32 gates 163 us with two, 213 with three; fp32
-// 202 and 294; bf16 alone 154 and 150).
+// Workgroups of a CU.  Three, whose registers hold the next tile as well; packed
+// tiles of 8 bytes an element would spill 9 of them (7 sequences, 32768 tokens of
+// 2048 channels: fp32 206 us with two, 209 with three; bf16 with fp32 gates 172
+// and 157, bf16 alone 149 and 137).
 template <class T, class G, bool PACKED>
-constexpr int per_cu() { return PACKED && sizeof(T) + sizeof(G) > 4 ? 2 : 3; }
+constexpr int per_cu() { return PACKED && sizeof(T) + sizeof(G) > 6 ? 2 : 3; }
 
 template <class T, class G, int VE, int FORM, bool PACKED>
 __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, G, PACKED>() : 4)) scan_fwd_kernel(ScanArgs a, Chain ch) {
@@ -65,12 +65,12 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
         const unsigned c = p.cb + l * VE, lane = g * K * D + c, c4 = c < D ? 4 * c : NOWHERE;
         const int64_t base = p.row * a.D;
         auto at = [&](int k, unsigned size) { return (c < D ? lane * size : NOWHERE) + k * D * size; };
-        float A[K][VE], U[K][VE], F[VE], R[VE];  // F, R: the factor of the group's map, and its complement (as in Joint)
+        float A[K][VE], U[K][VE], F[VE];  // F: the factor of the group's map
         const Rows<K, PACKED> rw = ahead;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             F[e] = 1.f;
-            R[e] = 0.f;
+            float rest = 0.f;  // its complement, as in Joint
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 float v = form.logits ? small_of_logit(gt[k][e]) : small_of_log(gt[k][e]);
@@ -78,19 +78,19 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
                 const float w = rest_of(v), u = form.comp ? w * x[k][e] : x[k][e];
                 A[k][e] = decay_of(v);
                 U[k][e] = PACKED ? (rw.live(k) ? u : 0.f) : u;  // x behind a sequence's end reads as zero
-                R[e] += w * F[e];
+                rest += w * F[e];
                 F[e] *= A[k][e];
                 settle(A[k][e]);
                 settle(U[k][e]);
             }
             settle(F[e]);
-            settle(R[e]);
+            s_rest[g][Q::place(l, e)] = rest;
         }
         const bool edges = PACKED && rw.edges();
         float h0 = 0.f;
         if (!PACKED && p.step == 0) {  // what the chain starts from
             h0 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer<float>(a.s0, p.sequence * a.D, a.s0 ? D : 0),
-                                                                     4 * (p.cb + Q::channel(jc)), 0, 0));
+                                                                     4 * (p.cb + Q::channel(anew(jc))), 0, 0));
             settle(h0);  // not waited for elsewhere
         }
         LookBack<Q::LOOK> back;
@@ -128,10 +128,7 @@ __global__ void __launch_bounds__((lanes_of<VE, PACKED>()), (VE > 1 ? per_cu<T, 
                     cu[e] = rw.first(k) ? U[k][e] : u;
                 }
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                s_map[g][Q::place(l, e)] = make_float2(PACKED ? with_mark(F[e], starts) : F[e], cu[e]);
-                s_rest[g][Q::place(l, e)] = R[e];
-            }
+            for (int e = 0; e < VE; ++e) s_map[g][Q::place(l, e)] = make_float2(PACKED ? with_mark(F[e], starts) : F[e], cu[e]);
         }
         __syncthreads();
         if (jp == 0) s_take[0] = __builtin_amdgcn_readfirstlane(next);

@@ -129,6 +129,13 @@ struct Lanes {
     static __device__ __forceinline__ int channel(int q) { return q % LPR * VE + q / LPR; }
 };
 
+// A lane's place, worked out again where it is used: what follows from it is
+// otherwise held in registers, or in scratch, over all tiles.
+__device__ __forceinline__ int anew(int place) {
+    asm volatile("" : "+v"(place));
+    return place;
+}
+
 // The form, compiled in or from the request.
 template <int FORM>
 struct Form {
@@ -245,11 +252,11 @@ __device__ __forceinline__ float with_mark(float value, bool cut) {
 }
 __device__ __forceinline__ bool has_mark(float value) { return __float_as_int(value) < 0; }
 
-// A channel's word: (factor, addend) of a map, or (anything, state).
-__device__ __forceinline__ void leave(uint64_t *p, float a, float u) {
+// Word `at` behind uniform ones: (factor, addend) of a map, or (anything, state).
+__device__ __forceinline__ void leave(uint64_t *words, unsigned at, float a, float u) {
     unsigned hi = __float_as_uint(u);
     if (hi == 0xffffffffu) hi = 0x7fc00000u;  // a NaN like any other: NOT_YET stays apart
-    __hip_atomic_store(p, static_cast<uint64_t>(hi) << 32 | __float_as_uint(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(words + at, static_cast<uint64_t>(hi) << 32 | __float_as_uint(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ float2 word(uint64_t w) {
     return make_float2(__uint_as_float(static_cast<unsigned>(w)), __uint_as_float(static_cast<unsigned>(w >> 32)));
@@ -259,14 +266,14 @@ __device__ __forceinline__ float2 word(uint64_t w) {
 // part jp of the words).  All but `w` is the same in all lanes of a wave.
 template <int LOOK>
 struct Look {
-    const uint64_t *words;
+    uint64_t *words;
     int n, first;  // words wanted, the lane's first
     uint64_t w[LOOK];
     __device__ __forceinline__ bool want(int k) const { return first + k < n; }
     // A first look, long before the words are needed.  No branch around its
     // loads, so that the loads behind them need not be waited for with them:
     // where there are no words it reads zeros.
-    __device__ __forceinline__ void start(const uint64_t *from, int count, int jc, int jp) {
+    __device__ __forceinline__ void start(uint64_t *from, int count, int jc, int jp) {
         words = from;
         n = count;
         first = jp * LOOK;
@@ -338,7 +345,7 @@ __device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, in
                                        float start, float2 (&s_maps)[PARTS][CW], float2 (&s_runs)[PARTS][CW], float (&s_start)[CW]) {
     if (jp == 0 && step + 1 < ch.tiles) {
         if (step == 0) own = make_float2(0.f, pass<PACKED>(own, start));
-        leave(ch.maps + (chain * ch.tiles + step) * CW + jc, own.x, own.y);
+        leave(back.maps.words, step % RUN * CW + jc, own.x, own.y);
     }
     back.maps.wait(ch, jc);
     s_maps[jp][jc] = back.maps.template map<PACKED>();
@@ -351,10 +358,10 @@ __device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, in
             for (int i = 0; i < PARTS; ++i) m.then(s_maps[i][jc]);
             m.then(own);
             const float2 run = m.map();
-            leave(ch.runs + (chain * (ch.tiles / RUN) + step / RUN) * CW + jc, run.x, run.y);
+            leave(back.runs.words, step % SPAN / RUN * CW + jc, run.x, run.y);
         }
         back.runs.wait(ch, jc);
-        s_runs[jp][jc] = back.runs.template map<PACKED>();
+        s_runs[jp][anew(jc)] = back.runs.template map<PACKED>();
         if (jp == 0 && step >= SPAN) {
             back.state.wait(ch, jc);
             s_start[jc] = word(back.state.w[0]).y;
@@ -370,7 +377,7 @@ __device__ __forceinline__ float enter(const Chain &ch, LookBack<LOOK> &back, in
     return h;
 }
 __device__ __forceinline__ void leave_state(const Chain &ch, int64_t chain, int step, int jc, float h) {
-    if (step % SPAN == SPAN - 1 && step + 1 < ch.tiles) leave(ch.states + (chain * (ch.tiles / SPAN) + step / SPAN) * CW + jc, 0.f, h);
+    if (step % SPAN == SPAN - 1 && step + 1 < ch.tiles) leave(ch.states + (chain * (ch.tiles / SPAN) + step / SPAN) * CW, jc, 0.f, h);
 }
 
 // No lane of the kernels branches by itself while a tile is in registers: what

@@ -56,13 +56,19 @@ def moves_of_some_lanes(lines):
     return found
 
 
+def spills(assembly):
+    """Registers of each kernel that do not fit: (in scratch memory, moved to accumulation registers)."""
+    kernel = r"\.agpr_count: +(\d+).*?\.name: +(\w+).*?\.vgpr_spill_count: +(\d+)"
+    return {m[1]: (int(m[2]), int(m[0])) for m in re.findall(kernel, assembly, re.S)}
+
+
 @pytest.fixture(scope="module")
 def assembly():
     def one(src):
         cmd = [build.HIPCC, *build.FLAGS, "-S", "--cuda-device-only", src, "-o", "-"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         assert r.returncode == 0, r.stderr[-4000:]
-        return os.path.basename(src), dict(functions(r.stdout))
+        return os.path.basename(src), (dict(functions(r.stdout)), spills(r.stdout))
 
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
         return dict(ex.map(one, build.sources()))
@@ -79,13 +85,20 @@ def test_the_reading_of_assembly():
 
 
 def test_no_register_is_moved_away_for_some_lanes(assembly):
-    bad = {f"{src}: {name}": m[0] for src, fs in assembly.items() for name, lines in fs.items() if (m := moves_of_some_lanes(lines))}
+    bad = {f"{src}: {name}": m[0] for src, (fs, _) in assembly.items() for name, lines in fs.items() if (m := moves_of_some_lanes(lines))}
     assert not bad, bad
 
 
 @pytest.mark.parametrize("source", ["scan_fwd.hip", "scan_bwd.hip"])
 def test_no_lane_of_the_scan_branches_by_itself(assembly, source):
-    kernels = {n: lines for n, lines in assembly[source].items() if "_kernel" in n}
+    kernels = {n: lines for n, lines in assembly[source][0].items() if "_kernel" in n}
     assert len(kernels) == 40  # 4 combinations of types, packed or not, 1 channel a lane or 8 in four forms
     bad = {n: m[0] for n, lines in kernels.items() if (m := mask_writes(lines))}
     assert not bad, bad
+
+
+@pytest.mark.parametrize("source", ["scan_fwd.hip", "scan_bwd.hip", "scan.hip", "rotary.hip"])
+def test_registers_suffice(assembly, source):
+    kernels, counts = {n for n in assembly[source][0] if "_kernel" in n}, assembly[source][1]
+    assert kernels == set(counts)
+    assert not {n: c for n, c in counts.items() if c != (0, 0)}
