@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
                     far = r < rows && !(ss > 0x1p-80f && ss < 0x1p100f);
                     const float m = a.l2 ? ss : ss * per + a.eps;
                     rs = __builtin_amdgcn_rsqf(m);
-                    rs = m > 0.f ? rs * (1.5f - 0.5f * m * rs * rs) : 0.f;  // 0: no row
+                    // 0: no row, whose mean is eps alone (a row that is not far has more than 2^-90)
+                    rs = m > 0x1p-100f ? rs * (1.5f - 0.5f * m * rs * rs) : 0.f;
                     if (__builtin_amdgcn_ballot_w64(far) != 0) {
                         double sum = 0.0;
 #pragma unroll
