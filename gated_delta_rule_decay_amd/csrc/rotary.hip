@@ -36,6 +36,7 @@ constexpr int NTH = 256;
 // rotated: 188 us with 2, 192 with 4, 201 with 8; 32768 of them normed: 109, 115,
 // 163; backward 163 with 1 or 2, 314 with 4, which spill.)
 constexpr int ROUNDS = 2;
+constexpr int IN_FP32 = 32;     // rows of a lane that a weight's gradient sums in fp32
 constexpr int MAX_TOKENS = 16;  // tokens of a workgroup
 constexpr int MAX_PAIRS = 128;
 
@@ -167,6 +168,7 @@ __device__ __forceinline__ int quotient(unsigned n, unsigned m) { return m ? __u
 template <class T, int VE, bool VEC, bool INTER, int MODE>
 __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4) rotary_kernel(RotaryArgs a, Shape sh, float *part) {
     __shared__ float s_cos[MAX_TOKENS][MAX_PAIRS + 8], s_sin[MAX_TOKENS][MAX_PAIRS + 8];
+    __shared__ double s_dw[NTH / 64][MODE == ROTARY_NORM_BWD ? 256 : 1];  // each wave's sums of dw
     const int which = blockIdx.x >= static_cast<unsigned>(sh.grid[0]);
     const int block = which ? blockIdx.x - sh.grid[0] : blockIdx.x;
     const RotaryPart pt = a.part[which];
@@ -189,6 +191,35 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
             }
         }
     }
+
+    // The lane groups' sums of dw, joined in order and added to the wave's in 64 bits:
+    // fp32 sums of a thousand equal terms were off by 1e-5 of themselves.  Each
+    // channel is one lane's.
+    // Joins the lane groups' sums of dw in order and adds them to the wave's, in 64
+    // bits: a thousand equal terms that a lane summed in fp32 were off by 1e-5 of
+    // their sum.  (1 us of 161 for 32768 tokens of 2 x 16 heads of 128.)  A channel is one
+    // lane's, so that no lane waits for another.
+    const bool sums = MODE == ROTARY_NORM_BWD && pt.dw;
+    int held = 0;       // rows in dw0 and dw1
+    bool fresh = true;  // nothing in s_dw yet
+    auto put_away = [&] {
+        int lane = threadIdx.x;
+        asm volatile("" : "+v"(lane));  // places worked out here, not held over the rows
+        double *at = s_dw[lane >> 6];
+        const bool mine = (lane & 63) < L && p.live;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            for (int o = L; o < 64; o <<= 1) {
+                dw0[e] += __shfl_xor(dw0[e], o);
+                dw1[e] += __shfl_xor(dw1[e], o);
+            }
+            if (mine && own0<INTER>(p, e, d, rot)) at[p.c0 + e] = (fresh ? 0.0 : at[p.c0 + e]) + dw0[e];
+            if (mine && own1<INTER>(p, e, d, rot)) at[p.c1 + e] = (fresh ? 0.0 : at[p.c1 + e]) + dw1[e];
+            dw0[e] = dw1[e] = 0.f;
+        }
+        held = 0;
+        fresh = false;
+    };
 
     for (int64_t tile = block; tile < sh.tiles[which]; tile += sh.grid[which]) {
         const int t0 = static_cast<int>(tile * TT), nt = a.tokens - t0 < TT ? a.tokens - t0 : TT;
@@ -329,30 +360,16 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
                 }
                 store_two<T, VE, VEC, INTER>(by, r * d * static_cast<unsigned>(sizeof(T)), static_cast<T *>(pt.y) + out + r * d, p, d, rot, on, u, v);
             }
+            if (sums && (held += ROUNDS) >= IN_FP32) put_away();
         }
     }
 
     if constexpr (MODE == ROTARY_NORM_BWD) {
-        // the lane groups' shares of dw, added up in order; one row a workgroup
-        if (!pt.dw) return;
-        float *red = &s_cos[0][0];  // [4][d], at most 4 x 256
-        static_assert(sizeof(s_cos) >= 4 * 256 * sizeof(float), "red fits");
+        if (!sums) return;
+        put_away();
         __syncthreads();
-        const int wave = threadIdx.x >> 6;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            for (int o = L; o < 64; o <<= 1) {
-                dw0[e] += __shfl_xor(dw0[e], o);
-                dw1[e] += __shfl_xor(dw1[e], o);
-            }
-            if ((threadIdx.x & 63) < static_cast<unsigned>(L) && p.live) {
-                if (own0<INTER>(p, e, d, rot)) red[wave * d + p.c0 + e] = dw0[e];
-                if (own1<INTER>(p, e, d, rot)) red[wave * d + p.c1 + e] = dw1[e];
-            }
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < d; c += NTH)
-            part[static_cast<int64_t>(blockIdx.x) * d + c] = (red[c] + red[d + c]) + (red[2 * d + c] + red[3 * d + c]);
+        for (int c = threadIdx.x; c < d; c += NTH)  // one row a workgroup
+            part[static_cast<int64_t>(blockIdx.x) * d + c] = static_cast<float>((s_dw[0][c] + s_dw[1][c]) + (s_dw[2][c] + s_dw[3][c]));
     }
 }
 

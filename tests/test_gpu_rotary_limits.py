@@ -37,3 +37,35 @@ def test_eps_below_normal_numbers(g, eps, d, dtype):
             dx, dw, bx, bw = ref.norm_turn_backward(dq, q, w, f, None, 0, False, 1.0, "rms", eps)
             ref.check("dq", r["dq"], dx, bx)
             ref.check("d_q_weight", r["d_q_weight"], dw, bw)
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_weight_sums_over_very_many_rows(g, norm):
+    # a thousand rows for each lane of the launch, and terms that do not change, so that
+    # roundings of one lane's sum would all go to the same side
+    T, d = 4 * 1024 * 1000 + 3, 255
+    q, dq = 1 + rn(d).abs(), 1 + rn(d, seed=1).abs()
+    w = 1 + 0.1 * rn(d, seed=2)
+    f = torch.zeros(1, dtype=F64, device="cuda")
+    r = g.qk_norm_rotary_bwd(dq.expand(T, 1, d).contiguous(), None, q.expand(T, 1, d).contiguous(), None, w, None, f, norm=norm)
+    dx, dw, bx, bw = ref.norm_turn_backward(dq.expand(1, 1, d), q.expand(1, 1, d), w, f, None, 0, False, 1.0, norm, 1e-6)
+    ref.check("d_q_weight", r["d_q_weight"], T * dw, T * bw)
+    for first in (0, T - 5):
+        ref.check("dq", r["dq"][first:first + 5], dx.expand(5, 1, d), bx.expand(5, 1, d))
+
+
+def test_weight_sums_of_k_and_of_wide_vectors(g):
+    # some hundred rows a lane, eight bf16 channels a vector, q and k apart; the sums over rows in parts
+    T, Hq, Hk, d = 200000, 24, 8, 64
+    q, dq = torch.randn(T, Hq, d, dtype=BF, device="cuda") + 1, torch.randn(T, Hq, d, dtype=BF, device="cuda") + 1
+    k, dk = torch.randn(T, Hk, d, dtype=BF, device="cuda") - 1, torch.randn(T, Hk, d, dtype=BF, device="cuda") + 1
+    w = 1 + 0.1 * rn(d, seed=2)
+    r = g.qk_norm_rotary_bwd(dq, dk, q, k, w, w, norm="l2")
+    for n, x, dy in (("q", q, dq), ("k", k, dk)):
+        want, bound = torch.zeros(d, dtype=F64, device="cuda"), torch.zeros(d, dtype=F64, device="cuda")
+        for a, b in zip(x.split(20000), dy.split(20000)):
+            a, b = a.double(), b.double()
+            t = b * (a / a.norm(dim=-1, keepdim=True))
+            want += t.sum((0, 1))
+            bound += 72 * ref.E * t.abs().sum((0, 1))
+        ref.check(f"d_{n}_weight", r[f"d_{n}_weight"], want.cpu(), bound.cpu())
