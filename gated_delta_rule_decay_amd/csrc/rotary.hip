@@ -16,10 +16,10 @@
 // backward in 158 us, 5.1 TB/s.  256 tokens take 4 us on the GPU, 9 from call to
 // call, which the host needs for one.
 //
-// Angles: p f / 2 pi in fp64 (53 bits; a position of 2^20 leaves 2^-33 turns),
-// the nearest quarter turn taken off exactly, then the Taylor series of sine
-// and cosine on [-pi/4, pi/4] in fp32, whose first terms left out are below
-// 2^-28.  Everything else is fp32, rounded once at the end; a row whose sum of
+// Angles: p f / 2 pi from products of 106 bits, so that the farthest positions have
+// their part of a turn to 2^-50 as the first ones do, the nearest quarter turn
+// taken off exactly, then the Taylor series of sine and cosine on [-pi/4, pi/4] in
+// fp32, whose first terms left out are below 2^-28.  Everything else is fp32, rounded once at the end; a row whose sum of
 // squares leaves [2^-80, 2^100] is summed and scaled in fp64 instead, so that no
 // row of finite values overflows or vanishes.
 #include <type_traits>
@@ -40,9 +40,20 @@ constexpr int IN_FP32 = 32;     // rows of a lane that a weight's gradient sums 
 constexpr int MAX_TOKENS = 16;  // tokens of a workgroup
 constexpr int MAX_PAIRS = 128;
 
-// cos and sin of 2 pi t
+// Turns of p f / 2 pi, less whole ones: the product and what its rounding left
+// out, times 1 / 2 pi to 106 bits.  (Of the product alone a position of 2^40 keeps 12
+// bits of a radian.)
+__device__ __forceinline__ double turns_of(double p, double f) {
+#pragma clang fp contract(off)
+    constexpr double INV = 0x1.45f306dc9c883p-3, REST = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    const double a = p * f, b = __builtin_fma(p, f, -a), q = a * INV;
+    const double left = __builtin_fma(a, INV, -q) + (a * REST + b * INV);
+    const double t = (q - rint(q)) + left;
+    return t - rint(t);
+}
+
+// cos and sin of 2 pi t, |t| <= 1/2
 __device__ __forceinline__ void cos_sin_turns(double t, float &c, float &s) {
-    t -= rint(t);
     const double n = rint(4.0 * t);
     const float x = 6.283185307179586f * static_cast<float>(t - 0.25 * n), y = x * x;
     const float sn = x + x * y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880))));
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
                     int at = first + t;
                     if (at >= a.period) at = a.period < MAX_TOKENS ? at % a.period : at - a.period;
                     float c = 0.f, s = 0.f;  // behind the last pair
-                    if (j < half) cos_sin_turns((offset + (a.pos ? a.pos[at] : at)) * (a.freq[j] * 0.15915494309189535), c, s);
+                    if (j < half) cos_sin_turns(turns_of(offset + (a.pos ? a.pos[at] : at), a.freq[j]), c, s);
                     s_cos[t][j] = a.cos_mag * c;
                     s_sin[t][j] = a.sin_mag * s;
                 }

@@ -563,7 +563,8 @@ gdn2_status gdn2_layer_norm_bwd(const gdn2_norm_desc *desc, const void *dy, cons
  *     offset + r % period                (positions NULL)
  * so period = tokens gives every token its own and period = T with tokens =
  * B * T shares them among the batch.  freq: device fp64 [rotary/2], radians a
- * position; angles are formed in 64 bits, so far positions lose nothing.
+ * position; an angle keeps its part of a turn to 2^-50 for up to 2^50 turns, so
+ * far positions lose nothing.
  * Arithmetic is fp32 (a norm's sum of squares that leaves [2^-80, 2^100], and
  * its 1/r, fp64: values of any size), results are rounded once.  A row of zeros
  * without eps stays zero.

@@ -69,3 +69,55 @@ def test_weight_sums_of_k_and_of_wide_vectors(g):
             want += t.sum((0, 1))
             bound += 72 * ref.E * t.abs().sum((0, 1))
         ref.check(f"d_{n}_weight", r[f"d_{n}_weight"], want.cpu(), bound.cpu())
+
+
+def far_angles(positions, freq):
+    """cos and sin of position * freq, the product reduced in integers."""
+    bits = 300
+
+    def arctan_of_inverse(n):
+        term = total = (1 << bits) // n
+        k, sign = 1, 1
+        while term:
+            term //= n * n
+            k, sign = k + 2, -sign
+            total += sign * (term // k)
+        return total
+
+    two_pi = 8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))  # Machin's formula, times 2^bits
+    c, s = (torch.empty(len(positions), 1, len(freq), dtype=F64) for _ in range(2))
+    for i, p in enumerate(positions):
+        for j, f in enumerate(freq):
+            top, bottom = f.as_integer_ratio()  # a power of 2 below
+            rest = ((p * top << bits) // bottom) % two_pi  # radians times 2^bits
+            t = torch.tensor(rest / (1 << bits), dtype=F64)
+            c[i, 0, j], s[i, 0, j] = t.cos(), t.sin()
+    return c, s
+
+
+@pytest.mark.parametrize("offset", [0, -(1 << 40), (1 << 40) - 3, 123456789012, 1 << 24])
+@pytest.mark.parametrize("inter", [False, True])
+def test_angles_of_far_positions(g, inter, offset):
+    # the bounds are those of near positions: angles lose nothing on the way
+    d, positions = 16, [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 131071, 77777777]
+    f = torch.tensor([0.7499, 1.0, 1 / 3, 0.1 ** 0.5, 1e-3, 2.5, 1e-9, 3.999], dtype=F64)
+    q, k = rn(len(positions), 2, d), rn(len(positions), 1, d, seed=1)
+    pos = torch.tensor(positions, dtype=torch.int32).cuda()
+    c, s = far_angles([offset + p for p in positions], f.tolist())
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if inter else (slice(0, d // 2), slice(d // 2, d))
+    for back, fn in ((1, g.rotary_fwd), (-1, g.rotary_bwd)):
+        for x, y in zip((q, k), fn(q, k, f.cuda(), positions=pos, offset=offset, interleaved=inter)):
+            x = x.cpu().double()
+            want, size = torch.empty_like(x), torch.empty_like(x)
+            u, v = x[..., a], x[..., b]
+            want[..., a], want[..., b] = c * u - back * s * v, back * s * u + c * v
+            size[..., a] = size[..., b] = u.abs() + v.abs()
+            ref.check("x", y, want, 9 * ref.E * size)
+    y = g.qk_norm_rotary_fwd(q, None, freq=f.cuda(), positions=pos, offset=offset, interleaved=inter)[0]
+    h = q.cpu().double()
+    h = h / (h.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    u, v = h[..., a], h[..., b]
+    want, size = torch.empty_like(h), torch.empty_like(h)
+    want[..., a], want[..., b] = c * u - s * v, s * u + c * v
+    size[..., a] = size[..., b] = u.abs() + v.abs()
+    ref.check("normed", y, want, 24 * ref.E * size)
