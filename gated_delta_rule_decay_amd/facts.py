@@ -19,6 +19,12 @@ def facts(t):
         raise TypeError(f"expected a torch.Tensor, not {type(t).__name__}") from None
 
 
+def needed(f, name):
+    """Raises where a tensor that the call cannot do without is None."""
+    if f is None:
+        raise TypeError(f"{name} must be a torch.Tensor, not None")
+
+
 def contiguous(shape, stride):
     step = 1
     for n, s in zip(reversed(shape), reversed(stride)):

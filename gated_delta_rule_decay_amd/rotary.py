@@ -11,7 +11,7 @@ import functools
 import math
 
 from .binding import GDN2_BF16, GDN2_F32
-from .facts import contiguous, facts, like, new_like
+from .facts import contiguous, facts, like, needed, new_like
 from .linear import _bytes, _ptr, _register, _run, _space
 
 GDN2_ROTARY_HALF, GDN2_ROTARY_INTERLEAVED = 0, 1
@@ -113,6 +113,7 @@ def _type_code(dtype, name):
 def _request(names, q, k, freq, positions, q_weight, k_weight, interleaved, magnitude, norm, eps):
     """The descriptor (offset 0) of checked facts."""
     import torch
+    needed(q, names[0])
     shape, _, dtype, dev = q
     if len(shape) < 3:
         raise ValueError(f"{names[0]} is [..., H, d] with at least one token axis")
@@ -163,10 +164,10 @@ def _plan(q, k, freq, positions, offset, interleaved, magnitude, norm=GDN2_QK_NO
 
 
 def _out(given, name, x):
-    if x is None:
-        return None
     if given is None:
-        return new_like(x)
+        return None if x is None else new_like(x)
+    if x is None:
+        raise ValueError(f"{name} has nothing to hold")
     like(facts(given), name, x.shape, (x.dtype,), x.device)
     return given
 
@@ -244,9 +245,9 @@ def qk_norm_rotary_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, fre
     desc = _plan(q, k, freq, positions, offset, interleaved, magnitude, _norm_code(norm), eps, q_weight, k_weight)
     dev = q.device
     for g, x, n in ((d_q_out, q, "d_q_out"), (d_k_out, k, "d_k_out")):
+        if (x is None) != (g is None):
+            raise ValueError(f"{n} is missing" if g is None else f"{n} has no input")
         if x is not None:
-            if g is None:
-                raise ValueError(f"{n} is missing")
             like(facts(g), n, x.shape, (q.dtype,), dev)
     dq, dk = _out(None, "dq", q), _out(None, "dk", k)
     dqw = None if q_weight is None else new_like(q_weight)
@@ -254,6 +255,6 @@ def qk_norm_rotary_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, fre
     ws, n = None, 0
     if dqw is not None or dkw is not None or workspace is not None:
         ws, n = _space(workspace, _sum_bytes(desc.tokens, desc.q_heads, desc.k_heads, desc.dim, desc.rotary, desc.dtype), dev)
-    _run("gdn2_qk_norm_bwd", dev, desc, _ptr(d_q_out), _ptr(d_k_out) if k is not None else None, _ptr(q), _ptr(k), _ptr(q_weight),
+    _run("gdn2_qk_norm_bwd", dev, desc, _ptr(d_q_out), _ptr(d_k_out), _ptr(q), _ptr(k), _ptr(q_weight),
          _ptr(k_weight), _ptr(freq), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(ws), n)
     return dict(dq=dq, dk=dk, d_q_weight=dqw, d_k_weight=dkw)

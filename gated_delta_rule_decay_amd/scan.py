@@ -10,7 +10,7 @@ import ctypes
 import functools
 
 from .binding import GDN2_BF16, GDN2_F32
-from .facts import facts, like, new_like
+from .facts import facts, like, needed, new_like
 from .linear import _bytes, _ptr, _register, _run, _space
 from .rotary import _type_code
 
@@ -60,6 +60,8 @@ def _request(kind, x, log_decay, cu_seqlens, gate_logits, complement, states, *t
     tensors [N,D] fp32 and of tensors like x, None among the facts skipped.
     """
     import torch
+    needed(x, "x")
+    needed(log_decay, "log_decay")
     shape, _, dtype, dev = x
     packed = cu_seqlens is not None
     if kind == "step":
@@ -93,6 +95,11 @@ def _request(kind, x, log_decay, cu_seqlens, gate_logits, complement, states, *t
     n = (T + SCAN_MARK - 1) // SCAN_MARK
     need = 0 if kind == "step" else _bytes(f"gdn2_scan_{kind}{'_varlen' if packed else ''}_workspace", desc)
     return desc, need, N, (n, D) if packed else (shape[0], n, D)
+
+
+def _offsets(cu_seqlens):
+    if cu_seqlens is None:  # which stands for whole sequences within
+        raise ValueError("cu_seqlens is missing")
 
 
 def _fwd(x, log_decay, cu_seqlens, state0, gate_logits, complement, out, state_out, return_state, return_marks, workspace):
@@ -138,15 +145,19 @@ def gated_scan_fwd_varlen(x, log_decay, cu_seqlens, state0=None, gate_logits=Fal
     device; states [N,D]; marks [ceil(T/128),D].  Tokens outside every sequence
     are not written: a given ``out`` keeps them, a new one has any value there.
     """
+    _offsets(cu_seqlens)
     return _fwd(x, log_decay, cu_seqlens, state0, gate_logits, complement, out, state_out, return_state, return_marks, workspace)
 
 
 def _bwd(dy, x, log_decay, marks, cu_seqlens, state0, d_state, gate_logits, complement, want_state0, workspace):
     import torch
+    needed(dy, "dy")
     desc, need, N, mshape = _request("bwd", facts(x), facts(log_decay), facts(cu_seqlens), bool(gate_logits), bool(complement),
                                      (("state0", facts(state0)), ("d_state", facts(d_state))), ("dy", facts(dy)))
     dev, f32 = x.device, torch.float32
-    like(facts(marks), "marks", mshape, (f32,), dev)
+    fm = facts(marks)
+    needed(fm, "marks")
+    like(fm, "marks", mshape, (f32,), dev)
     if want_state0 is None:
         want_state0 = state0 is not None
     dx, dg = new_like(x), new_like(log_decay)
@@ -180,6 +191,7 @@ def gated_scan_bwd_varlen(dy, x, log_decay, marks, cu_seqlens, state0=None, d_st
 
     Gradients of tokens outside every sequence are not written (any value).
     """
+    _offsets(cu_seqlens)
     return _bwd(dy, x, log_decay, marks, cu_seqlens, state0, d_state, gate_logits, complement, want_state0, workspace)
 
 
@@ -188,6 +200,7 @@ def gated_scan_step(x, log_decay, state, gate_logits=False, complement=False, ou
 
     x, log_decay [N,D] as for ``gated_scan_fwd``.  Returns y like x.
     """
+    needed(state, "state")
     desc, _, _, _ = _request("step", facts(x), facts(log_decay), None, bool(gate_logits), bool(complement),
                              (("state", facts(state)),), ("out", facts(out)))
     if out is None:
