@@ -11,9 +11,9 @@
 // half layout channels j and rot/2 + j, so that both members of its pairs are
 // in one lane, else neighbouring ones.  A workgroup takes some tokens of q or
 // of k; its lanes form each (token, pair) angle once, in LDS, for all heads.
-// With 2 x 16 heads of 128 bf16 channels (a large copy: 5.14 TB/s): 65536 tokens
-// turned in 186 us, 5.8 TB/s; 32768 normed and turned in 104 us, 5.1 TB/s,
-// backward in 158 us, 5.1 TB/s.  256 tokens take 4 us on the GPU, 9 from call to
+// With 2 x 16 heads of 128 bf16 channels (a large copy: 5.0 to 5.5 TB/s): 65536 tokens
+// turned in 186 us, 5.8 TB/s; 32768 normed and turned in 106 us, 5.0 TB/s,
+// backward in 160 us, 5.0 TB/s.  256 tokens take 4 us on the GPU, 9 from call to
 // call, which the host needs for one.
 //
 // Angles: p f / 2 pi from products of 106 bits, so that the farthest positions have
@@ -444,8 +444,8 @@ Shape shape_of(const RotaryArgs &a, int ve) {
 // Whether rows are whole aligned vectors: channels, pair blocks and strides in
 // units of VE, every pointer on 16 bytes.  Rows that are not go element by
 // element (8 x 4096 tokens of 2 x 16 heads of 128 bf16 channels from an odd
-// address: rotation 238 us, with the norm 260, backward 461; aligned 95, 104 and
-// 158).
+// address: rotation 231 us, with the norm 260, backward 482; aligned 93, 106 and
+// 160).
 bool vector_ok(const RotaryArgs &a) {
     const int ve = a.bf16 ? 8 : 4;
     if (a.d % ve || a.rot % (2 * ve)) return false;

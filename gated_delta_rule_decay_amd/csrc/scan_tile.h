@@ -13,14 +13,14 @@
 // are composed over LDS; the state that enters the tile comes from the tiles
 // before it, and the lane then runs its tokens once more.  So every element is
 // read once.  Rows that are not whole aligned vectors of 8 go element by element
-// (8 x 4096 tokens of 2048 bf16 channels from an odd address: forward 121 us,
-// backward 251; aligned 96 and 149).
+// (8 x 4096 tokens of 2048 bf16 channels from an odd address: forward 125 us,
+// backward 232; aligned 98 and 148).
 //
 // Bound by HBM where there are many chains; where there are few, by how long a
 // word takes from one workgroup to another, twice a tile: its run's maps, and the
-// run before.  (That forward moves 405 MB in 96 us, 4.2 TB/s, the backward 673 MB
-// in 149 us, 4.5 TB/s, a large copy 5.14 TB/s; one sequence of 65536 tokens takes
-// 277 us, 3.9 TB/s, and 222 if nothing is waited for.)
+// run before.  (That forward moves 405 MB in 98 us, 4.1 TB/s, the backward 673 MB
+// in 148 us, 4.5 TB/s, a large copy 5.0 to 5.5 TB/s; one sequence of 65536 tokens
+// takes 284 us, 3.8 TB/s, of which its waits are about a fifth.)
 //
 // Between tiles (a chain: the tiles of one block of channels of one sequence):
 // a tile leaves its map as one 64-bit word a channel, both halves and the fact
@@ -32,12 +32,14 @@
 // takes its tiles from a counter, along the chain, works on them in that order,
 // and a tile waits only for tiles that the counter gave out before it: the first
 // tile that is not done is at work, and the wait ends.  (It is bounded all the
-// same, for calls that share a workspace at the same time, which is not allowed.)
+// same, for calls that share a workspace at the same time, which is not allowed.
+// A word that has not come by then counts as it stands, and that is NaN in both
+// halves, so what depends on it is NaN.)
 //
 // Packed sequences are one axis with resets: at a sequence's first token the
 // state comes from state0, (-0, a s0 + u), and backward the gradient that enters
 // a sequence's last token from behind is d_state_out's.  A factor of -0, which no
-// decay has, takes nothing of what is before it, be it infinite, NaN or the mark
+// other map has, takes nothing of what is before it, be it infinite, NaN or the mark
 // of a row of no sequence.  What a token is comes from a table of sequence
 // indices, one a token, built on the device.
 #pragma once
@@ -380,8 +382,10 @@ __device__ __forceinline__ void leave_state(const Chain &ch, int64_t chain, int 
     if (step % SPAN == SPAN - 1 && step + 1 < ch.tiles) leave(ch.states + (chain * (ch.tiles / SPAN) + step / SPAN) * CW, jc, 0.f, h);
 }
 
-// No lane of the kernels branches by itself while a tile is in registers: what
-// a lane does not need goes to NOWHERE, and branches are those of whole waves.
+// No lane of the kernels branches by itself: what a lane does not need goes to
+// NOWHERE, and branches are those of whole waves.  (Where registers are short the
+// compiler has moved live values away behind a branch of some lanes before it
+// turned the others back on, and they lost theirs.)
 
 // An offset, or nowhere.  (By its top bit, which no offset has: of a ?: the
 // compiler makes a branch where it is used more than once.)
