@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
     // channel is one lane's.
     // Joins the lane groups' sums of dw in order and adds them to the wave's, in 64
     // bits: a thousand equal terms that a lane summed in fp32 were off by 1e-5 of
-    // their sum.  (1 us of 161 for 32768 tokens of 2 x 16 heads of 128.)  A channel is one
-    // lane's, so that no lane waits for another.
+    // their sum.  (32768 tokens of 2 x 16 heads of 128 take 160 us either way, from odd
+    // addresses 481 for 459.)  A channel is one lane's, so that none waits for another.
     const bool sums = MODE == ROTARY_NORM_BWD && pt.dw;
     int held = 0;       // rows in dw0 and dw1
     bool fresh = true;  // nothing in s_dw yet
@@ -218,12 +218,14 @@ __global__ void __launch_bounds__(NTH, MODE == ROTARY_NORM_BWD && VE > 4 ? 3 : 4
         asm volatile("" : "+v"(lane));  // places worked out here, not held over the rows
         double *at = s_dw[lane >> 6];
         const bool mine = (lane & 63) < L && p.live;
+        for (int o = L; o < 64; o <<= 1)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            for (int o = L; o < 64; o <<= 1) {
+            for (int e = 0; e < VE; ++e) {
                 dw0[e] += __shfl_xor(dw0[e], o);
                 dw1[e] += __shfl_xor(dw1[e], o);
             }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
             if (mine && own0<INTER>(p, e, d, rot)) at[p.c0 + e] = (fresh ? 0.0 : at[p.c0 + e]) + dw0[e];
             if (mine && own1<INTER>(p, e, d, rot)) at[p.c1 + e] = (fresh ? 0.0 : at[p.c1 + e]) + dw1[e];
             dw0[e] = dw1[e] = 0.f;
